@@ -18,6 +18,11 @@ package is its thin Python binding.  Functions carry the C names:
   WRITE_SCALAR, DECAY_NONE, ERASE_NONE, WRITE_NONE), and the input prologue (QK_L2NORM: raw q, k
   normalised in the call; BW_LOGITS: b, w given as logits)
 * ``gdn2_prologue``: the input prologue alone (normalised q, k; sigmoid gates)
+* ``gdn2_qk_rope`` / ``gdn2_qk_rope_bwd``: per-head RMS norm of q and k with the rotation by position
+* ``gdn2_attn_fwd`` / ``gdn2_attn_bwd`` and their ``_varlen`` forms: causal attention with grouped heads
+  and an optional sliding window, for the attention layers of a hybrid stack
+* ``gdn2_cache_write`` / ``gdn2_cache_read``: a paged key-value cache, bf16 or e4m3
+* ``gdn2_attn_cached``: attention of the newest tokens over the paged cache
 * ``gdn2_workspace_size``, ``gdn2_sync_status``, ``gdn2_strerror``
 
 The library is loaded lazily by ``load()``; a missing library raises.
@@ -28,3 +33,7 @@ from ._lib import (EXPORTS, GDN2_BF16, GDN2_F32, GDN2_OK, LIB_PATH, NOALLOC_MAX_
                    gdn2_decode_step_gated, gdn2_workspace_size_gated, DECAY_SCALAR, ERASE_SCALAR, WRITE_SCALAR,
                    DECAY_NONE, ERASE_NONE, WRITE_NONE, QK_L2NORM, BW_LOGITS, gdn2_decode_step, gdn2_prologue, gdn2_chunk_fwd_save, gdn2_chunk_bwd_saved, gdn2_chunk_fwd_host, gdn2_strerror, gdn2_sync_status, gdn2_selftest_timeout,
                    gdn2_workspace_size, load, raw)
+from ._attn import (CACHE_BF16, CACHE_E4M3, ROPE_INTERLEAVED, ROPE_RMSNORM, gdn2_attn_bwd,  # noqa: F401
+                    gdn2_attn_bwd_varlen, gdn2_attn_cached, gdn2_attn_cached_workspace_size, gdn2_attn_fwd,
+                    gdn2_attn_fwd_varlen, gdn2_attn_workspace_size, gdn2_cache_read, gdn2_cache_write, gdn2_qk_rope,
+                    gdn2_qk_rope_bwd)

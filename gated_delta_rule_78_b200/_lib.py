@@ -19,13 +19,16 @@ GDN2_OK = 0
 STATUS_NAMES = {0: "GDN2_OK", -1: "GDN2_ERR_NULL", -2: "GDN2_ERR_SHAPE", -3: "GDN2_ERR_DTYPE",
                 -4: "GDN2_ERR_ALIGN", -5: "GDN2_ERR_WORKSPACE", -6: "GDN2_ERR_CUDA",
                 -7: "GDN2_ERR_TIMEOUT", -8: "GDN2_ERR_UNSUPPORTED", -9: "GDN2_ERR_TOO_LARGE",
-                -10: "GDN2_ERR_SEQLENS"}
+                -10: "GDN2_ERR_SEQLENS", -11: "GDN2_ERR_PAGES"}
 GDN2_F32, GDN2_BF16 = 0, 1
 EXPORTS = ("gdn2_chunk_fwd", "gdn2_decode_step", "gdn2_chunk_bwd", "gdn2_workspace_size",
            "gdn2_strerror", "gdn2_sync_status", "gdn2_chunk_bwd_noalloc", "gdn2_chunk_fwd_varlen",
            "gdn2_chunk_bwd_varlen", "gdn2_chunk_fwd_gated", "gdn2_chunk_bwd_gated", "gdn2_decode_step_gated",
            "gdn2_workspace_size_gated", "gdn2_prologue", "gdn2_chunk_fwd_save", "gdn2_chunk_bwd_saved",
-           "gdn2_chunk_fwd_host", "gdn2_selftest_timeout")
+           "gdn2_chunk_fwd_host", "gdn2_selftest_timeout", "gdn2_qk_rope", "gdn2_qk_rope_bwd",
+           "gdn2_qk_rope_workspace_size", "gdn2_attn_fwd", "gdn2_attn_fwd_varlen", "gdn2_attn_bwd",
+           "gdn2_attn_bwd_varlen", "gdn2_attn_workspace_size", "gdn2_cache_write", "gdn2_cache_read",
+           "gdn2_attn_cached", "gdn2_attn_cached_workspace_size")
 # gate layout flags (gdn2_gate_flags in include/gdn2.h)
 DECAY_SCALAR, ERASE_SCALAR, WRITE_SCALAR, DECAY_NONE, ERASE_NONE, WRITE_NONE = 1, 2, 4, 8, 16, 32
 # input prologue: q, k L2-normalised in the call; b, w given as logits (sigmoid in the call)
@@ -88,6 +91,30 @@ def load(path: str | None = None):
     lib.gdn2_strerror.restype = ctypes.c_char_p
     lib.gdn2_sync_status.argtypes = [vp]
     lib.gdn2_sync_status.restype = i
+    f = ctypes.c_float
+    lib.gdn2_qk_rope.argtypes = [i] * 7 + [vp] * 6 + [f, f] + [vp] * 3
+    lib.gdn2_qk_rope.restype = i
+    lib.gdn2_qk_rope_bwd.argtypes = [i] * 7 + [vp] * 6 + [f, f] + [vp] * 7 + [sz, vp]
+    lib.gdn2_qk_rope_bwd.restype = i
+    lib.gdn2_qk_rope_workspace_size.argtypes = [i] * 6
+    lib.gdn2_qk_rope_workspace_size.restype = sz
+    lib.gdn2_attn_fwd.argtypes = [i] * 7 + [f] + [vp] * 6
+    lib.gdn2_attn_fwd.restype = i
+    lib.gdn2_attn_fwd_varlen.argtypes = [i] * 7 + [f] + [vp] * 7
+    lib.gdn2_attn_fwd_varlen.restype = i
+    lib.gdn2_attn_bwd.argtypes = [i] * 7 + [f] + [vp] * 10 + [sz, vp]
+    lib.gdn2_attn_bwd.restype = i
+    lib.gdn2_attn_bwd_varlen.argtypes = [i] * 7 + [f] + [vp] * 11 + [sz, vp]
+    lib.gdn2_attn_bwd_varlen.restype = i
+    lib.gdn2_attn_workspace_size.argtypes = [i] * 6
+    lib.gdn2_attn_workspace_size.restype = sz
+    for fn in (lib.gdn2_cache_write, lib.gdn2_cache_read):
+        fn.argtypes = [i] * 6 + [vp] * 3 + [i] * 3 + [vp] * 7
+        fn.restype = i
+    lib.gdn2_attn_cached.argtypes = [i] * 8 + [f] + [vp] * 3 + [i] * 3 + [vp] * 8 + [sz, vp]
+    lib.gdn2_attn_cached.restype = i
+    lib.gdn2_attn_cached_workspace_size.argtypes = [i] * 9
+    lib.gdn2_attn_cached_workspace_size.restype = sz
     lib.gdn2_selftest_timeout.argtypes = [i, vp]
     lib.gdn2_selftest_timeout.restype = i
     _lib = lib

@@ -1,0 +1,490 @@
+// Attention of each sequence's newest tokens over the paged cache, few rows to a key head (decode
+// steps), and the joining of parts.
+//
+// A decode step reads every visible key and value once and computes 4 D flop a pair for the G query
+// heads of a key head: it is bound by memory.  A block takes 16 packed query rows (row r is token
+// r / G, head r % G) and one part of the key axis; its 4 warps take key steps of 16 in turn, each with
+// a ring of its own of cp.async stages, so that no warp waits for another until the end, where their
+// sums are joined in shared memory.  Products are m16n8k16 (16 rows are all there is: a 128-row tile
+// of the fifth-generation tensor core would be 7/8 empty and the time is the loads').  e4m3 rows go
+// to shared memory as they are and become bf16 in registers; a key's scale multiplies its score,
+// a value's scale its weight.
+//
+// Cut into parts, each part writes its normalised output and log-sum; a second kernel joins them,
+// in a fixed order.
+#include "attn_tc.cuh"
+
+namespace gdn2 {
+namespace {
+
+using attn::e4m3x4_bf16;
+using attn::ex2;
+using attn::kLn2;
+using attn::kLog2e;
+using tc::pack_bf16x2;
+using tc::smem_u32;
+
+constexpr int kWarps = 4, kRows = 16, kStep = 16;  // warps, query rows, keys of a warp's step
+constexpr float kGrow = 8.f;  // growth of the maximum (log2) that moves the reference
+
+template <int D, bool e4m3> struct Cfg {
+    static constexpr int ROW = D * (e4m3 ? 1 : 2);         // bytes of a cache row
+    static constexpr int TILE = kStep * ROW;               // a warp's K (or V) stage
+    static constexpr int SCALES = e4m3 ? 2 * kStep * 4 : 0;
+    static constexpr int STAGE = 2 * TILE + SCALES;
+    static constexpr int ST = e4m3 ? 4 : D == 128 ? 3 : 4;
+    static constexpr int RING = kWarps * ST * STAGE;
+    static constexpr int MERGE = kWarps * kRows * (D + 4) * 4;  // the warps' outputs, over the rings
+    static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+};
+
+struct Params {
+    SeqBatch b;
+    int H, Hkv, G, window, splits, piece;
+    float scale;
+    PagedCache c;
+    const __nv_bfloat16 *q;
+    __nv_bfloat16 *o;
+    float *lse, *part_o, *part_l;
+    int *status;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 16-byte chunk c of row r of a stage whose rows are 64, 128 or 256 bytes; the chunk index is
+// permuted by the row so that the 8 rows of an ldmatrix lie in different banks
+template <int ROW> __device__ __forceinline__ uint32_t chunk(int r, int c)
+{
+    if constexpr (ROW == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+    else return r * ROW + ((c ^ (r & 7)) << 4);
+}
+
+// Block x < n is the first tile of sequence x; the others are the further tiles of sequences with
+// more than 16 rows, in order.  By a whole warp.
+__device__ __forceinline__ bool find_rows(const Params &p, int x, TileRef &r)
+{
+    if (x < p.b.n) {
+        r.seq = x;
+        r.tile = 0;
+        r.sp = batch_span(p.b, x);
+        return r.sp.len > 0;
+    }
+    int e = x - p.b.n;
+    const int lane = threadIdx.x & 31;
+    for (int base = 0; base < p.b.n; base += 32) {
+        SeqSpan sp = {0, -1};
+        if (base + lane < p.b.n) sp = batch_span(p.b, base + lane);
+        const int more = sp.len > 0 ? (int)(((long long)sp.len * p.G + kRows - 1) / kRows) - 1 : 0;
+        int sum = more;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, m);
+            if (lane >= m) sum += v;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, sum > e);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            r.seq = base + src;
+            r.tile = 1 + e - __shfl_sync(0xffffffffu, sum - more, src);
+            r.sp.bos = __shfl_sync(0xffffffffu, sp.bos, src);
+            r.sp.len = __shfl_sync(0xffffffffu, sp.len, src);
+            return true;
+        }
+        e -= __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return false;
+}
+
+template <int D, bool e4m3>
+__global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_constant__ Params p)
+{
+    using C = Cfg<D, e4m3>;
+    extern __shared__ __align__(128) char sm[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 0) report_bad_seqlens(p.b, p.status);
+    TileRef r;
+    if (!find_rows(p, blockIdx.x, r)) return;
+    const int kvlen = p.c.kv_lens[r.seq], first = kvlen - r.sp.len;
+    if (first < 0 || kvlen > (long long)p.c.width * p.c.page) {
+        if (tid == 0) atomicExch(p.status, kStatusBadPages);
+        return;
+    }
+    const int hk = blockIdx.y, r0 = r.tile * kRows, rows = min(kRows, r.sp.len * p.G - r0);
+    // keys that this tile's rows see, and this block's part of them
+    const int low = first + r0 / p.G, high = first + (r0 + rows - 1) / p.G;
+    const int lo = p.window == 0 || low < p.window ? 0 : low - p.window + 1;
+    const int kb = lo + (int)blockIdx.z * p.piece, ke = min(high + 1, kb + p.piece);
+    const size_t part = (size_t)blockIdx.z * p.b.rows * p.H;
+    auto row_at = [&](int row) {  // [rows, H] index of the tile's row
+        const int rr = r0 + row, tok = rr / p.G;
+        return (size_t)(r.sp.bos + tok) * p.H + hk * p.G + (rr - tok * p.G);
+    };
+    if (kb >= ke) {  // nothing in this part
+        if (tid < rows) p.part_l[part + row_at(tid)] = -INFINITY;
+        return;
+    }
+
+    // Q fragments: rows g and g + 8.  e4m3 keys come four channels to a lane (see below), so there a
+    // lane's k indices 2t, 2t+1, 2t+8, 2t+9 stand for channels 4t .. 4t+3; a sum has no order.
+    uint32_t qf[D / 16][4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = g + 8 * i;
+        const __nv_bfloat16 *q = p.q + row_at(min(row, rows - 1)) * D;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                qf[k][i + 2 * e] = *reinterpret_cast<const uint32_t *>(q + 16 * k + (e4m3 ? 4 * t + 2 * e : 2 * t + 8 * e));
+    }
+    int pos[2];  // positions of this lane's two rows
+#pragma unroll
+    for (int i = 0; i < 2; ++i) pos[i] = g + 8 * i < rows ? first + (r0 + g + 8 * i) / p.G : -1;
+
+    const int *table = p.c.table + (size_t)r.seq * p.c.width;
+    char *ring = sm + warp * C::ST * C::STAGE;
+    const int nsteps = (ke - kb + kStep - 1) / kStep, mine = nsteps > warp ? (nsteps - warp + kWarps - 1) / kWarps : 0;
+    // keys kb + 16 (warp + 4 i) .. of this warp's step i into its stage i % ST; rows past the part and
+    // rows of bad pages become zeros
+    auto load = [&](int i) {
+        if (i < mine) {
+            const int at = kb + kStep * (warp + kWarps * i) + (lane & 15);
+            int slot = -1;
+            if (at < ke) {
+                const int pg = at / p.c.page, id = table[pg];
+                if (id >= 0 && id < p.c.num_pages) slot = id * p.c.page + (at - pg * p.c.page);
+                else atomicExch(p.status, kStatusBadPages);
+            }
+            char *st = ring + (i % C::ST) * C::STAGE;
+            constexpr int CH = C::ROW / 16, RP = 32 / CH;
+            const int ch = lane % CH;
+#pragma unroll
+            for (int x = 0; x < kStep / RP; ++x) {
+                const int row = x * RP + lane / CH, s = __shfl_sync(0xffffffffu, slot, row);
+                const size_t off = ((size_t)max(s, 0) * p.Hkv + hk) * C::ROW + ch * 16;
+                const uint32_t to = smem_u32(st) + chunk<C::ROW>(row, ch), n = s >= 0 ? 16 : 0;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"((const char *)p.c.k + off), "r"(n) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + C::TILE), "l"((const char *)p.c.v + off), "r"(n) : "memory");
+            }
+            if constexpr (e4m3) {  // lanes 0-15 the keys' scales, 16-31 the values'
+                const float *sc = (lane < 16 ? p.c.ks : p.c.vs) + (size_t)max(slot, 0) * p.Hkv + hk;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(st + 2 * C::TILE) + 4 * lane), "l"(sc), "r"(slot >= 0 ? 4 : 0) : "memory");
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < C::ST - 1; ++i) load(i);
+
+    float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    const float c = p.scale * kLog2e;
+    for (int i = 0; i < mine; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(C::ST - 2) : "memory");
+        __syncwarp();
+        load(i + C::ST - 1);
+        const uint32_t sk = smem_u32(ring + (i % C::ST) * C::STAGE), sv = sk + C::TILE;
+        float s[2][4] = {};
+        if constexpr (!e4m3) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                // matrices: keys 0-7 / 8-15 (lane bit 4) x channels 16k .. +7 / +8 .. +15 (lane bit 3)
+                uint32_t b[4];
+                ldm4(b, sk + chunk<C::ROW>((lane & 7) + (lane & 16) / 2, 2 * k + ((lane >> 3) & 1)));
+                mma_bf16(s[0], qf[k], b[0], b[1]);
+                mma_bf16(s[1], qf[k], b[2], b[3]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < D / 16; k += 2) {
+                // keys 0-7 / 8-15 (lane bit 3) x 16 channels of step k / k + 1 (lane bit 4): a lane
+                // gets channels 4t .. 4t + 3 of key g
+                uint32_t b[4], x, y;
+                ldm4(b, sk + chunk<C::ROW>((lane & 7) + (lane & 8), k + (lane >> 4)));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    e4m3x4_bf16(b[e], x, y);
+                    mma_bf16(s[e & 1], qf[k + (e >> 1)], x, y);
+                }
+            }
+        }
+        const float *sc = reinterpret_cast<const float *>(ring + (i % C::ST) * C::STAGE + 2 * C::TILE);
+        const int k0 = kb + kStep * (warp + kWarps * i) + 2 * t;
+        float top[2] = {m[0], m[1]};
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = k0 + 8 * n + (e & 1), at = pos[e >> 1];
+                if constexpr (e4m3) s[n][e] *= sc[8 * n + 2 * t + (e & 1)];
+                const bool vis = key <= at && key < ke && (p.window == 0 || key > at - p.window);
+                s[n][e] = vis ? s[n][e] : -INFINITY;
+                top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
+            }
+        bool grow[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+            grow[x] = (top[x] - m[x]) * c > kGrow;
+        }
+        if (__any_sync(0xffffffffu, grow[0] || grow[1])) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float f = grow[x] ? ex2((m[x] - top[x]) * c) : 1.f;
+                if (grow[x]) m[x] = top[x];
+                l[x] *= f;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    o[n][2 * x] *= f;
+                    o[n][2 * x + 1] *= f;
+                }
+            }
+        }
+        const float off[2] = {m[0] == -INFINITY ? 0.f : -m[0] * c, m[1] == -INFINITY ? 0.f : -m[1] * c};
+        uint32_t pf[4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float a = ex2(fmaf(s[n][2 * x], c, off[x])), b = ex2(fmaf(s[n][2 * x + 1], c, off[x]));
+                l[x] += a + b;
+                if constexpr (e4m3) {
+                    a *= sc[kStep + 8 * n + 2 * t];
+                    b *= sc[kStep + 8 * n + 2 * t + 1];
+                }
+                pf[x + 2 * n] = pack_bf16x2(a, b);
+            }
+#pragma unroll
+        for (int d = 0; d < D / 16; d += (e4m3 ? 2 : 1)) {
+            uint32_t b[4];
+            if constexpr (!e4m3) {
+                // keys 0-7 / 8-15 (lane bit 3) x 8 channels 2d / 2d + 1 (lane bit 4), transposed
+                ldm4t(b, sv + chunk<C::ROW>((lane & 7) + (lane & 8), 2 * d + (lane >> 4)));
+                mma_bf16(o[2 * d], pf, b[0], b[1]);
+                mma_bf16(o[2 * d + 1], pf, b[2], b[3]);
+            } else {
+                // 16 channels d / d + 1 in pairs of bytes: a lane gets channels 2g and 2g + 1 of keys
+                // 2t and 2t + 1, so output tile 2d holds the even channels of 16d .. and 2d + 1 the odd
+                ldm4t(b, sv + chunk<C::ROW>((lane & 7) + (lane & 8), d + (lane >> 4)));
+                uint32_t ev[4], od[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) e4m3x4_bf16(__byte_perm(b[e], 0, 0x3120), ev[e], od[e]);
+                mma_bf16(o[2 * d], pf, ev[0], ev[1]);
+                mma_bf16(o[2 * d + 1], pf, od[0], od[1]);
+                mma_bf16(o[2 * d + 2], pf, ev[2], ev[3]);
+                mma_bf16(o[2 * d + 3], pf, od[2], od[3]);
+            }
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+    }
+    // ---- the warps' sums joined: O and (m, l) of each warp over the rings
+    __syncthreads();
+    float *so = reinterpret_cast<float *>(sm);
+    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+    constexpr int OS = D + 4;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        float *dst = so + (warp * kRows + g + 8 * x) * OS;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+            if constexpr (!e4m3) {
+                *reinterpret_cast<float2 *>(dst + 16 * d + 2 * t) = make_float2(o[2 * d][2 * x], o[2 * d][2 * x + 1]);
+                *reinterpret_cast<float2 *>(dst + 16 * d + 8 + 2 * t) = make_float2(o[2 * d + 1][2 * x], o[2 * d + 1][2 * x + 1]);
+            } else {
+                *reinterpret_cast<float4 *>(dst + 16 * d + 4 * t) =
+                    make_float4(o[2 * d][2 * x], o[2 * d + 1][2 * x], o[2 * d][2 * x + 1], o[2 * d + 1][2 * x + 1]);
+            }
+        }
+        if (t == 0) {
+            s_m[warp][g + 8 * x] = m[x];
+            s_l[warp][g + 8 * x] = l[x];
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < rows * (D / 4); i += kWarps * 32) {
+        const int row = i / (D / 4), ch = i % (D / 4) * 4;
+        float top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][row]);
+        const float base = top == -INFINITY ? 0.f : top;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = ex2((s_m[w][row] - base) * c);
+            const float4 v = *reinterpret_cast<const float4 *>(so + (w * kRows + row) * OS + ch);
+            sum += f * s_l[w][row];
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+        }
+        const bool some = sum > 0.f || sum != sum;
+        const float inv = some ? 1.f / sum : 0.f, lse = some ? (top * c + __log2f(sum)) * kLn2 : -INFINITY;
+        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        const size_t at = row_at(row);
+        if (p.splits > 1) {
+            *reinterpret_cast<float4 *>(p.part_o + (part + at) * D + ch) = acc;
+            if (ch == 0) p.part_l[part + at] = lse;
+        } else {
+            *reinterpret_cast<uint2 *>(p.o + at * D + ch) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+            if (ch == 0 && p.lse) p.lse[at] = lse;
+        }
+    }
+}
+
+// o = sum_z 2^(lse_z - top) o_z / sum_z 2^(lse_z - top): a warp to a (token, head) row.  Rows of no
+// sequence, or of one that was skipped, are left as they are.
+template <int D> __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ Params p)
+{
+    const long long at = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const long long n = p.b.rows * p.H;
+    if (at >= n) return;
+    SeqSpan sp;
+    const int seq = find_seq(p.b, (int)(at / p.H), sp);
+    if (seq < 0) return;
+    const int kvlen = p.c.kv_lens[seq];
+    if (kvlen < sp.len || kvlen > (long long)p.c.width * p.c.page) return;
+    constexpr int E = D / 32;
+    float acc[E] = {}, top = -INFINITY, sum = 0.f;
+    for (int z = lane; z < p.splits; z += 32) top = fmaxf(top, p.part_l[(size_t)z * n + at]);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    for (int z0 = 0; z0 < p.splits; z0 += 32) {
+        const float mine = z0 + lane < p.splits ? p.part_l[(size_t)(z0 + lane) * n + at] : -INFINITY;
+        const float wt = mine == -INFINITY ? 0.f : ex2((mine - top) * kLog2e);  // NaN stays NaN
+        unsigned some = __ballot_sync(0xffffffffu, mine != -INFINITY);
+        sum += wt;
+        while (some) {
+            const int z = __ffs(some) - 1;
+            some &= some - 1;
+            const float f = __shfl_sync(0xffffffffu, wt, z);
+            const float *src = p.part_o + ((size_t)(z0 + z) * n + at) * D + lane * E;
+            if constexpr (E == 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(src);
+                acc[0] += f * v.x;
+                acc[1] += f * v.y;
+                acc[2] += f * v.z;
+                acc[3] += f * v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(src);
+                acc[0] += f * v.x;
+                acc[1] += f * v.y;
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    const bool any = sum > 0.f || sum != sum;
+    const float inv = any ? 1.f / sum : 0.f;
+    __nv_bfloat16 *dst = p.o + at * D + lane * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t *>(dst + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if (p.lse && lane == 0) p.lse[at] = any ? top + __log2f(sum) * kLn2 : -INFINITY;
+}
+
+template <int D, bool e4m3> cudaError_t run(const Params &p, dim3 grid, cudaStream_t s)
+{
+    auto kernel = attn_rows_kernel<D, e4m3>;
+    cudaError_t e = set_smem_attr(reinterpret_cast<const void *>(kernel), Cfg<D, e4m3>::SMEM);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kWarps * 32, Cfg<D, e4m3>::SMEM, s>>>(p);
+    return cudaGetLastError();
+}
+
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+}  // namespace
+
+CachedPlan cached_plan(int n, long long rows, int H, int Hkv, int window, long long capacity)
+{
+    const int G = H / Hkv;
+    CachedPlan plan;
+    // rows a sequence and key head, on average: up to 32 the step is bound by the cache's bytes
+    plan.tc = rows * G > 32LL * n;
+    const long long keys = window > 0 && window + rows < capacity ? window + rows : capacity;
+    if (plan.tc) {
+        const long long blocks = (rows * G / 256 + n) * Hkv;
+        const long long want = ceil_div(device_sms(), blocks);
+        plan.splits = (int)(want < keys / 512 ? want : keys / 512);
+    } else {
+        const long long blocks = (long long)n * Hkv;
+        long long want = ceil_div(4LL * device_sms(), blocks);
+        const long long even = ceil_div(keys, 2048);  // ragged lengths: no block reads more than 2048 keys
+        if (want < even) want = even;
+        plan.splits = (int)(want < keys / 256 ? want : keys / 256);
+    }
+    if (plan.splits > 256) plan.splits = 256;
+    if (plan.splits < 1) plan.splits = 1;
+    return plan;
+}
+
+size_t cached_workspace_bytes(long long rows, int H, int D, int splits)
+{
+    return splits > 1 ? (size_t)splits * rows * H * (D + 1) * sizeof(float) : 0;
+}
+
+cudaError_t launch_attn_cached(const CachedArgs &a, bool use_tc, cudaStream_t s)
+{
+    Params p{};
+    p.b = a.b;
+    p.H = a.H;
+    p.Hkv = a.Hkv;
+    p.G = a.H / a.Hkv;
+    p.window = a.window;
+    p.splits = a.splits;
+    p.scale = a.scale;
+    p.c = a.c;
+    p.q = (const __nv_bfloat16 *)a.q;
+    p.o = (__nv_bfloat16 *)a.o;
+    p.lse = a.lse;
+    p.part_o = a.part_o;
+    p.part_l = a.part_l;
+    p.status = a.status;
+    cudaError_t e;
+    if (use_tc) {
+        e = launch_attn_cached_tc(a, s);
+    } else {
+        long long keys = (long long)a.c.width * a.c.page;
+        if (a.window > 0 && a.window + kRows < keys) keys = a.window + kRows;
+        p.piece = ceil_div(ceil_div(keys, a.splits), kStep * kWarps) * kStep * kWarps;
+        const long long tiles = a.b.n + a.b.rows * p.G / kRows;
+        if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+        const dim3 grid((unsigned)tiles, (unsigned)a.Hkv, (unsigned)a.splits);
+        if (a.c.e4m3) e = a.D == 128 ? run<128, true>(p, grid, s) : run<64, true>(p, grid, s);
+        else e = a.D == 128 ? run<128, false>(p, grid, s) : run<64, false>(p, grid, s);
+    }
+    if (e != cudaSuccess || a.splits == 1) return e;
+    const unsigned blocks = (unsigned)((a.b.rows * a.H + 7) / 8);
+    (a.D == 128 ? attn_join_kernel<128> : attn_join_kernel<64>)<<<blocks, 256, 0, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn2

@@ -1,0 +1,110 @@
+// Pieces shared by the tensor-core attention kernels (attn_fwd_tc.cu, attn_bwd_tc.cu): tile sizes,
+// the packing of query rows, bounded waits, and the bf16 tiles' products.
+//
+// Query rows are packed by key head: row r of a tile of kBM rows is token r / G, query head r % G of
+// the G = H / Hkv heads that read one key head, so one key tile serves all of them (a tile holds
+// kTQ = kBM / G tokens; rows past kTQ * G are not used).  A packed tile arrives by one TMA box of
+// (64 channels, G heads, kTQ tokens) per 64 channels.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "attn.cuh"
+#include "tc_util.cuh"
+
+namespace gdn2 {
+namespace attn {
+
+constexpr int kBM = 128, kBN = 128;      // query rows and keys of a tile
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr int kBoxBytes = kBM * 128;     // 128 rows of 64 bf16 channels (one SW128 column block)
+
+// A bounded wait that every role of a block leaves once one of them has given up.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *abort, int *status)
+{
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = tc::global_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 16; ++i)
+            if (tc::mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if (tc::global_ns() - t0 > 2000000000ull) {
+            *abort = 1;
+            atomicExch(status, kStatusTimeout);
+            return false;
+        }
+    }
+}
+
+// ... by a whole warp, with one answer for all of its lanes
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *abort, int *status)
+{
+    return __all_sync(0xffffffffu, wait(bar, parity, abort, status));
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// D (128 x N, fp32, TMEM) (+)= A (128 x 16 ks) B^T: both operands K-major SW128 tiles of `rows`
+// rows in column blocks of 64, A in shared memory.
+template <int kSteps, int kRowsA, int kRowsB>
+__device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc)
+{
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks)
+        tc::mma_ss(d, tc::sdesc_sw128(a + (ks >> 2) * (kRowsA * 128) + (ks & 3) * 32, 16, 1024),
+                   tc::sdesc_sw128(b + (ks >> 2) * (kRowsB * 128) + (ks & 3) * 32, 16, 1024), idesc, acc || ks > 0);
+}
+// D (128 x N) (+)= A B with A (128 x 16 ks, bf16) in TMEM and B a tile [16 ks rows][N channels] in
+// shared memory, N-major: column blocks of 64 channels kRows * 128 bytes apart.
+template <int kSteps, int kRows>
+__device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc)
+{
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks)
+        tc::mma_ts(d, a + 8 * ks, tc::sdesc_sw128(b + ks * 2048, kRows * 128, 1024), idesc, acc || ks > 0);
+}
+
+// Zeros in rows [from, 128) of an SW128 tile of kBlocks column blocks, by one warp, visible to the
+// tensor core's reads that the warp issues afterwards.
+template <int kBlocks> __device__ __forceinline__ void zero_rows(char *tile, int from)
+{
+    const int lane = threadIdx.x & 31;
+    for (int i = from * 8 + lane; i < 128 * 8; i += 32)
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) *reinterpret_cast<uint4 *>(tile + b * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// Four e4m3 values as two pairs of bf16 (exact: e4m3 -> f16 -> f32 -> bf16).
+__device__ __forceinline__ void e4m3x4_bf16(uint32_t x, uint32_t &lo, uint32_t &hi)
+{
+    uint32_t h0, h1;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(h0), "=r"(h1)
+        : "r"(x));
+    const float2 f0 = __half22float2(*reinterpret_cast<const __half2 *>(&h0));
+    const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&h1));
+    lo = tc::pack_bf16x2(f0.x, f0.y);
+    hi = tc::pack_bf16x2(f1.x, f1.y);
+}
+
+// TMA view of a bf16 [rows][heads][D] tensor: boxes of (64 channels, box_heads, box_rows).
+bool make_head_map(CUtensorMap *m, const void *ptr, long long rows, int heads, int D, int box_heads, int box_rows);
+
+// 32 bytes in one store
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+}  // namespace attn
+}  // namespace gdn2

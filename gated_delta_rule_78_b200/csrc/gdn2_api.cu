@@ -290,6 +290,7 @@ const char *gdn2_strerror(gdn2_status s)
     case GDN2_ERR_TIMEOUT: return "a kernel gave up a bounded wait";
     case GDN2_ERR_UNSUPPORTED: return "outside the supported shapes (Dk == Dv in {64, 128})";
     case GDN2_ERR_TOO_LARGE: return "problem needs more scratch than the library's static array holds";
+    case GDN2_ERR_PAGES: return "kv_lens or block_table names a place outside the paged cache";
     case GDN2_ERR_SEQLENS: return "cu_seqlens is not 0 = c_0 <= c_1 <= ... <= c_N = total_T";
     }
     return "unknown status";
@@ -651,6 +652,7 @@ gdn2_status gdn2_sync_status(void *stream)
     if (v != 0) {
         const int zero = 0;
         if (cudaMemcpyToSymbol(g_gdn2_status, &zero, sizeof(int)) != cudaSuccess) return GDN2_ERR_CUDA;
+        if (v == gdn2::kStatusBadPages) return GDN2_ERR_PAGES;
         return v == gdn2::kStatusBadSeqlens ? GDN2_ERR_SEQLENS : GDN2_ERR_TIMEOUT;
     }
     return GDN2_OK;

@@ -14,6 +14,7 @@ constexpr int kChunk = 64;  // tokens per chunk
 
 // Device status word values (written by kernels, read by gdn2_sync_status).
 constexpr int kStatusTimeout = 1;
+constexpr int kStatusBadPages = 3;    // a block_table or kv_lens entry outside the paged cache
 constexpr int kStatusBadSeqlens = 2;  // cu_seqlens not non-decreasing inside [0, total_T]
 
 template <typename T> __device__ __forceinline__ float to_f(T x);

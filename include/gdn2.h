@@ -66,7 +66,9 @@ typedef enum {
     GDN2_ERR_UNSUPPORTED = -8, /* valid but outside the v1 shape contract */
     GDN2_ERR_TOO_LARGE = -9,   /* needs more scratch than GDN2_NOALLOC_MAX_SCRATCH_BYTES
                                   (gdn2_chunk_bwd_noalloc only) */
-    GDN2_ERR_SEQLENS = -10     /* a kernel found cu_seqlens invalid (reported by gdn2_sync_status) */
+    GDN2_ERR_SEQLENS = -10,    /* a kernel found cu_seqlens invalid (reported by gdn2_sync_status) */
+    GDN2_ERR_PAGES = -11       /* a kernel found a kv_lens or block_table entry outside the paged cache
+                                  (reported by gdn2_sync_status) */
 } gdn2_status;
 
 typedef enum { GDN2_F32 = 0, GDN2_BF16 = 1 } gdn2_dtype;
@@ -313,6 +315,130 @@ GDN2_API gdn2_status gdn2_prologue(int flags, gdn2_dtype dt, int N, int H, int D
                                    const void *b, const void *w, void *q_n, void *k_n, void *b_s, void *w_s,
                                    void *stream);
 
+/*
+ * The attention layer of a hybrid stack.
+ *
+ * The method's hybrid stacks interleave the recurrent layers above with sliding-window attention
+ * layers (aixai.ru, the evaluation section: a 2K window).  The calls below make such a layer: a
+ * per-head norm and rotation of q and k, causal attention for training and prompts, and a paged
+ * cache with the attention that reads it for serving.  The conventions at the top of this file
+ * hold, with these additions:
+ *  - q and o have H heads, k and v Hkv heads; for attention Hkv divides H, H / Hkv <= 64, and query
+ *    head h reads key head h / (H / Hkv).  One head size D in {64, 128}.  Rows x heads < 2^31.
+ *  - Packed batches: cu_seqlens, DEVICE int32 [N + 1], 0 = c_0 <= c_1 <= ... <= c_N <= total_T.
+ *    Empty sequences are allowed; rows behind c_N belong to no sequence and the outputs' rows there
+ *    are left as they were (a padded batch).  A sequence whose entries are invalid is skipped, its
+ *    outputs left as they were, and GDN2_ERR_SEQLENS recorded.
+ *  - q, k, v and d_o of a sequence are expected to be finite.  A value that is not may reach the
+ *    outputs of any token of its own sequence, those that mask it included, but never those of
+ *    another sequence; what lies behind a sequence in its last page is never used.
+ *  - Every result is the same from call to call, bit for bit: no sum depends on timing.
+ */
+
+/*
+ * Per-head RMS norm and rotation by position, in one pass.  For each of N token rows and each head
+ * of q [N, H, D] and k [N, Hkv, D] (here H and Hkv are any two counts):
+ *   n = x / sqrt(mean x^2 + eps) * weight     with GDN2_ROPE_RMSNORM; n = x without
+ *   y = n with its first `rot` channels rotated in pairs (a, b) by the angle pos * inv_freq[i]:
+ *       (a, b) -> rot_scale * (a cos - b sin, b cos + a sin)
+ * Pair i is (i, i + rot / 2), or (2i, 2i + 1) with GDN2_ROPE_INTERLEAVED; i < rot / 2.
+ *   rot: even, 0 .. D (0: no rotation, positions and inv_freq are ignored).
+ *   q_weight, k_weight: fp32 [D], or NULL for ones (ignored without GDN2_ROPE_RMSNORM).
+ *   positions: int32 [N].  inv_freq: fp32 [rot / 2]; a context extension is a choice of inv_freq and
+ *   rot_scale.  The angle is formed in 64 bits, so positions may be far.
+ * q_out may be q and k_out k.  Asynchronous on `stream`.
+ * The backward takes the gradients of q_out and k_out and the forward's inputs, and writes dq, dk and
+ * the fp32 weight gradients [D] (each may be NULL: not wanted).  Without GDN2_ROPE_RMSNORM q, k and the
+ * weight gradients are ignored.  dq may be d_q_out and dk d_k_out.  Workspace:
+ * gdn2_qk_rope_workspace_size() bytes when a weight gradient is wanted, else NULL is accepted.
+ */
+typedef enum { GDN2_ROPE_RMSNORM = 1, GDN2_ROPE_INTERLEAVED = 2 } gdn2_rope_flags;
+
+GDN2_API gdn2_status gdn2_qk_rope(int flags, gdn2_dtype dt, int N, int H, int Hkv, int D, int rot, const void *q,
+                                  const void *k, const float *q_weight, const float *k_weight, const int *positions,
+                                  const float *inv_freq, float eps, float rot_scale, void *q_out, void *k_out,
+                                  void *stream);
+GDN2_API gdn2_status gdn2_qk_rope_bwd(int flags, gdn2_dtype dt, int N, int H, int Hkv, int D, int rot, const void *q,
+                                      const void *k, const float *q_weight, const float *k_weight,
+                                      const int *positions, const float *inv_freq, float eps, float rot_scale,
+                                      const void *d_q_out, const void *d_k_out, void *dq, void *dk, float *dq_weight,
+                                      float *dk_weight, void *workspace, size_t ws_bytes, void *stream);
+GDN2_API size_t gdn2_qk_rope_workspace_size(int flags, gdn2_dtype dt, int N, int H, int Hkv, int D);
+
+/*
+ * Causal attention over whole sequences.  The query at position i of its sequence sees the keys
+ * j <= i, with window > 0 only those with j > i - window (window = 0: all of them):
+ *   s_ij = scale q_i . k_j,  p_ij = e^(s_ij - lse_i),  lse_i = ln sum_j e^(s_ij),  o_i = sum_j p_ij v_j
+ *   q, o: [B, T, H, D]; k, v: [B, T, Hkv, D] of type dt (packed: [total_T, ..]); scale > 0.
+ *   lse: fp32 [B, T, H], or NULL when not wanted.
+ * bf16 runs on the tensor cores (fp32 scores, sums and accumulators; the weights p rounded to bf16
+ * for the second product), fp32 in fp32 throughout.
+ * The backward of L = <o, d_o>, given the forward's inputs, o and lse:
+ *   dq, dk, dv as q, k, v; gradients of a key head are sums over its query heads.
+ *   workspace: gdn2_attn_workspace_size() bytes (packed: N = 1, T = total_T).
+ */
+GDN2_API gdn2_status gdn2_attn_fwd(gdn2_dtype dt, int B, int T, int H, int Hkv, int D, int window, float scale,
+                                   const void *q, const void *k, const void *v, void *o, float *lse, void *stream);
+GDN2_API gdn2_status gdn2_attn_fwd_varlen(gdn2_dtype dt, int N, int total_T, int H, int Hkv, int D, int window,
+                                          float scale, const int *cu_seqlens, const void *q, const void *k,
+                                          const void *v, void *o, float *lse, void *stream);
+GDN2_API gdn2_status gdn2_attn_bwd(gdn2_dtype dt, int B, int T, int H, int Hkv, int D, int window, float scale,
+                                   const void *q, const void *k, const void *v, const void *o, const float *lse,
+                                   const void *d_o, void *dq, void *dk, void *dv, void *workspace, size_t ws_bytes,
+                                   void *stream);
+GDN2_API gdn2_status gdn2_attn_bwd_varlen(gdn2_dtype dt, int N, int total_T, int H, int Hkv, int D, int window,
+                                          float scale, const int *cu_seqlens, const void *q, const void *k,
+                                          const void *v, const void *o, const float *lse, const void *d_o, void *dq,
+                                          void *dk, void *dv, void *workspace, size_t ws_bytes, void *stream);
+GDN2_API size_t gdn2_attn_workspace_size(gdn2_dtype dt, int N, int T, int H, int Hkv, int D);
+
+/*
+ * The paged cache.  k_cache, v_cache: [num_pages, page_size, Hkv, D], bf16 or e4m3 (one byte); e4m3
+ * has fp32 scales [num_pages, page_size, Hkv] for keys and for values.
+ *   block_table: DEVICE int32 [N, max_pages]; position p of sequence n is row p % page_size of page
+ *                block_table[n][p / page_size].  Entries past a sequence's length are not read.
+ *   kv_lens:     DEVICE int32 [N], the sequence's length WITH its new tokens: the rows that
+ *                cu_seqlens gives sequence n are its positions kv_lens[n] - (c_{n+1} - c_n) ..
+ *                kv_lens[n] - 1.
+ * dt is GDN2_BF16 (GDN2_F32 gives GDN2_ERR_UNSUPPORTED).  A page size is any number >= 1;
+ * max_pages * page_size <= 2^30, num_pages * page_size < 2^31.  A kv_lens entry below the sequence's
+ * new tokens or above max_pages * page_size skips the sequence, a page outside the cache skips the
+ * row (attention reads zeros for it), and either records GDN2_ERR_PAGES.
+ *
+ * gdn2_cache_write stores the new tokens' k and v [total_T, Hkv, D]; gdn2_cache_read reads the same
+ * rows back into k and v (with longer spans in cu_seqlens: a sequence's whole past).
+ *   e4m3: scale = amax / 448 over the row's finite channels, value = x / scale rounded to nearest
+ *   even; read back as bf16(value * scale).  A row of zeros has scale 0.  An infinity or NaN reads
+ *   back as NaN and leaves the other channels of its row alone.
+ * Two rows of one call that name the same place race; the library does not look for that.
+ */
+typedef enum { GDN2_CACHE_BF16 = 0, GDN2_CACHE_E4M3 = 1 } gdn2_cache_type;
+
+GDN2_API gdn2_status gdn2_cache_write(gdn2_cache_type type, gdn2_dtype dt, int N, int total_T, int Hkv, int D,
+                                      const int *cu_seqlens, const int *kv_lens, const int *block_table, int max_pages,
+                                      int num_pages, int page_size, const void *k, const void *v, void *k_cache,
+                                      void *v_cache, float *k_scale, float *v_scale, void *stream);
+GDN2_API gdn2_status gdn2_cache_read(gdn2_cache_type type, gdn2_dtype dt, int N, int total_T, int Hkv, int D,
+                                     const int *cu_seqlens, const int *kv_lens, const int *block_table, int max_pages,
+                                     int num_pages, int page_size, const void *k_cache, const void *v_cache,
+                                     const float *k_scale, const float *v_scale, void *k, void *v, void *stream);
+
+/*
+ * Attention of each sequence's newest tokens (one for a decode step, a chunk of a long prompt) over
+ * the paged cache, which already holds them.  q, o: [total_T, H, D]; lse: fp32 [total_T, H] or NULL.
+ * The query at position i sees the cached positions j <= i (and j > i - window), as gdn2_attn_fwd.
+ *   workspace: gdn2_attn_cached_workspace_size() bytes; 0 needs none (NULL allowed).  The calls that
+ *   share one must be ordered, captured graphs among them.
+ */
+GDN2_API gdn2_status gdn2_attn_cached(gdn2_cache_type type, gdn2_dtype dt, int N, int total_T, int H, int Hkv, int D,
+                                      int window, float scale, const int *cu_seqlens, const int *kv_lens,
+                                      const int *block_table, int max_pages, int num_pages, int page_size,
+                                      const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                      const float *v_scale, void *o, float *lse, void *workspace, size_t ws_bytes,
+                                      void *stream);
+GDN2_API size_t gdn2_attn_cached_workspace_size(gdn2_dtype dt, int N, int total_T, int H, int Hkv, int D, int window,
+                                                int max_pages, int page_size);
+
 /* Workspace bytes for which = 0 (gdn2_chunk_fwd), 1 (gdn2_chunk_bwd),
  * 2 (gdn2_chunk_fwd_varlen), 3 (gdn2_chunk_bwd_varlen, B = N, T = total_T) or
  * 4 (gdn2_chunk_fwd_host's device staging); 0 for invalid or unsupported arguments. */
@@ -323,7 +449,8 @@ GDN2_API const char *gdn2_strerror(gdn2_status status);
 
 /* Synchronises `stream`, then returns and clears the current device's kernel
  * status word: GDN2_ERR_TIMEOUT if a kernel gave up a bounded wait since the
- * last check, GDN2_ERR_SEQLENS if a kernel found cu_seqlens invalid,
+ * last check, GDN2_ERR_SEQLENS if a kernel found cu_seqlens invalid, GDN2_ERR_PAGES
+ * if one found a kv_lens or block_table entry outside the paged cache,
  * GDN2_ERR_CUDA if the stream reported an error, else GDN2_OK. */
 GDN2_API gdn2_status gdn2_sync_status(void *stream);
 

@@ -1,0 +1,248 @@
+"""The paged cache and the attention that reads it, against the 64-bit forms."""
+import random
+
+import pytest
+import torch
+
+import attn_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+class Batch:
+    """Sequences over a paged cache whose unused rows and scales hold NaN."""
+
+    def __init__(self, q_lens, kv_lens, page, Hkv, D, e4m3, seed=0, tail=0, slack=2):
+        g = torch.Generator().manual_seed(seed)
+        order = random.Random(seed)
+        self.q_lens, self.kv, self.page, self.Hkv, self.D, self.e4m3 = q_lens, kv_lens, page, Hkv, D, e4m3
+        need = [-(-n // page) for n in kv_lens]
+        pages = sum(need) + slack
+        ids = list(range(pages))
+        order.shuffle(ids)
+        width = max(need + [1]) + 1
+        self.table = torch.full((len(kv_lens), width), -5, dtype=torch.int32)
+        at = 0
+        for i, n in enumerate(need):
+            self.table[i, :n] = torch.tensor(ids[at:at + n], dtype=torch.int32)
+            at += n
+        self.total = sum(q_lens) + tail
+        self.k_all = [torch.randn(n, Hkv, D, generator=g).bfloat16() for n in kv_lens]
+        self.v_all = [torch.randn(n, Hkv, D, generator=g).bfloat16() for n in kv_lens]
+        shape = (pages, page, Hkv, D)
+        self.kc, self.vc = torch.full(shape, float("nan")).bfloat16(), torch.full(shape, float("nan")).bfloat16()
+        self.ks = self.vs = None
+        if e4m3:
+            self.kc, self.vc = self.kc.to(torch.float8_e4m3fn), self.vc.to(torch.float8_e4m3fn)
+            self.ks, self.vs = torch.full(shape[:3], float("nan")), torch.full(shape[:3], float("nan"))
+        self.cu = R.lens_to_cu(q_lens)
+        self.dev = {n: getattr(self, n).cuda() for n in ("table", "kc", "vc", "cu")}
+        self.dev["kv"] = torch.tensor(kv_lens, dtype=torch.int32).cuda()
+        self.dev["ks"], self.dev["vs"] = (None, None) if not e4m3 else (self.ks.cuda(), self.vs.cuda())
+
+    def args(self):
+        d = self.dev
+        return (d["cu"], d["kv"], d["table"], d["ks"], d["vs"])
+
+    def fill(self, g):
+        """Everything into the cache: the past in one call, then the new tokens in another."""
+        for part in ("past", "new"):
+            lens = [n - m if part == "past" else m for n, m in zip(self.kv, self.q_lens)]
+            ends = [n - m if part == "past" else n for n, m in zip(self.kv, self.q_lens)]
+            if sum(lens) == 0:
+                continue
+            pick = lambda xs: torch.cat([x[e - n:e] for x, n, e in zip(xs, lens, ends)]).cuda()  # noqa: E731
+            d = self.dev
+            g.gdn2_cache_write(pick(self.k_all), pick(self.v_all), d["kc"], d["vc"], R.lens_to_cu(lens).cuda(),
+                               torch.tensor(ends, dtype=torch.int32).cuda(), d["table"], d["ks"], d["vs"])
+        return self
+
+    def held(self, i):
+        """Sequence i's keys and values as the cache holds them, in 64 bits."""
+        if not self.e4m3:
+            return self.k_all[i].double(), self.v_all[i].double()
+        return tuple(y * s.double()[..., None] for y, s in (R.quantise(x[i]) for x in (self.k_all, self.v_all)))
+
+
+KINDS = [False, True]
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page,Hkv", [(1, 1), (16, 3), (48, 2), (64, 8), (7, 5)])
+def test_write_and_read(cuda_lib, page, Hkv, D, e4m3):
+    g = cuda_lib
+    b = Batch([1, 0, 40, 17, 3], [1, 9, 100, 17, 60], page, Hkv, D, e4m3, seed=page).fill(g)
+    d = b.dev
+    # everything of every sequence
+    cu = R.lens_to_cu(b.kv).cuda()
+    k, v = g.gdn2_cache_read(d["kc"], d["vc"], cu, d["kv"], d["table"], d["ks"], d["vs"], total_T=sum(b.kv))
+    assert g.gdn2_sync_status() == 0
+    want = [torch.cat(x) for x in zip(*[b.held(i) for i in range(len(b.kv))])]
+    for got, ref in zip((k, v), want):
+        if e4m3:
+            # the scale and the division are rounded in fp32, which moves a value to the neighbouring
+            # e4m3 step only next to a border; then bf16's half step of the product, on both sides
+            exact = ref.to(torch.float32).to(torch.bfloat16)
+            assert torch.equal(got.cpu(), exact)
+        else:
+            assert torch.equal(got.cpu().double(), ref)
+
+
+def test_e4m3_edges(cuda_lib):
+    """Zero rows, the largest values, subnormal quotients, ties, infinities and NaN."""
+    g = cuda_lib
+    rows = torch.zeros(8, 1, 64)
+    rows[1, 0, 0] = 448
+    rows[1, 0, 1:9] = torch.tensor([17.0, 19.0, 2.0 ** -9, 2.0 ** -10, 3 * 2.0 ** -10, -1.0625, -1.1875, 232.0])
+    rows[2] = 1e30
+    rows[3, 0, :3] = torch.tensor([float("inf"), 2.0, float("nan")])
+    rows[4] = float("nan")
+    rows[5, 0, 0] = 1e-38
+    rows[6] = 3.3e38
+    rows[7, 0, 5] = -5
+    rows = rows.bfloat16()
+    b = Batch([8], [8], 4, 1, 64, True)
+    b.k_all, b.v_all = [rows], [rows.flip(0)]
+    b.fill(g)
+    d = b.dev
+    k, v = g.gdn2_cache_read(d["kc"], d["vc"], *b.args(), total_T=8)
+    assert g.gdn2_sync_status() == 0
+    for got, x in ((k, rows), (v, rows.flip(0))):
+        y, s = R.quantise(x)
+        ref = (y * s.double()[..., None]).float().bfloat16()
+        assert torch.equal(torch.isnan(got.cpu()), torch.isnan(ref))
+        assert torch.equal(torch.nan_to_num(got.cpu()), torch.nan_to_num(ref))
+
+
+def attend(g, b, H, window=0, scale=0.11, seed=0, workspace=None):
+    gen = torch.Generator().manual_seed(seed)
+    q = torch.randn(b.total, H, b.D, generator=gen).bfloat16()
+    d = b.dev
+    o = torch.full(q.shape, 7.0).bfloat16().cuda()
+    lse = torch.full(q.shape[:2], 7.0).cuda()
+    g.gdn2_attn_cached(q.cuda(), d["kc"], d["vc"], *b.args(), window=window, scale=scale, o=o, lse=lse, workspace=workspace)
+    assert g.gdn2_sync_status() == 0
+    return q, o, lse
+
+
+def verify(b, q, o, lse, H, window, scale):
+    G, at = H // b.Hkv, 0
+    for i, (n, kv) in enumerate(zip(b.q_lens, b.kv)):
+        k, v = b.held(i)
+        for h in range(H):
+            if n == 0:
+                continue
+            x = R.head(q[at:at + n, h], k[:, h // G], v[:, h // G], kv - n, window, scale, torch.bfloat16)
+            R.check(o[at:at + n, h], x["o"], x["o_tol"], f"o of sequence {i} head {h}")
+            R.check(lse[at:at + n, h], x["lse"], x["lse_tol"], f"lse of sequence {i} head {h}")
+        at += n
+    assert (o[at:] == 7.0).all() and (lse[at:] == 7.0).all()
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_lens,kv_lens", [
+    ([1], [1]), ([1, 1, 1], [5, 64, 700]), ([1, 0, 2, 3], [333, 0, 2, 40]), ([5, 1], [5, 600]),
+])
+def test_decode(cuda_lib, q_lens, kv_lens, D, e4m3):
+    b = Batch(q_lens, kv_lens, 16, 2, D, e4m3, seed=sum(kv_lens), tail=2).fill(cuda_lib)
+    verify(b, *attend(cuda_lib, b, 8), 8, 0, 0.11)
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_lens,kv_lens,page", [
+    ([70], [70], 64), ([130, 1], [130, 900], 16), ([64, 300], [500, 301], 48), ([200, 0, 90], [1000, 3, 129], 256),
+])
+def test_chunks(cuda_lib, q_lens, kv_lens, page, D, e4m3):
+    b = Batch(q_lens, kv_lens, page, 2, D, e4m3, seed=sum(kv_lens) + 1, tail=3).fill(cuda_lib)
+    verify(b, *attend(cuda_lib, b, 8), 8, 0, 0.11)
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 1), (40, 2), (64, 1), (14, 2)])
+@pytest.mark.parametrize("rows", [1, 45])
+def test_heads(cuda_lib, rows, H, Hkv, e4m3):
+    b = Batch([rows, 1], [rows + 150, 77], 32, Hkv, 64, e4m3, seed=H).fill(cuda_lib)
+    verify(b, *attend(cuda_lib, b, H), H, 0, 0.11)
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+@pytest.mark.parametrize("window", [1, 16, 100, 2 ** 31 - 1])
+@pytest.mark.parametrize("rows", [1, 3, 150])
+def test_windows(cuda_lib, rows, window, e4m3):
+    b = Batch([rows, 1], [rows + 700, 1000], 16, 2, 128, e4m3, seed=window % 89).fill(cuda_lib)
+    verify(b, *attend(cuda_lib, b, 4, window=window), 4, window, 0.11)
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+@pytest.mark.parametrize("rows", [1, 40])
+def test_long_axis_in_parts(cuda_lib, rows, e4m3):
+    """One sequence, few rows: the key axis is cut into parts that a second kernel joins."""
+    g = cuda_lib
+    b = Batch([rows], [6001], 16, 1, 128, e4m3, seed=5).fill(g)
+    assert g.gdn2_attn_cached_workspace_size(1, rows, 4, 1, 128, 0, b.table.shape[1], 16) > 0
+    verify(b, *attend(g, b, 4), 4, 0, 0.11)
+
+
+def test_page_sizes(cuda_lib):
+    for page in (1, 3, 8, 128, 1000):
+        for rows in (1, 80):
+            b = Batch([rows], [rows + 300], page, 1, 64, False, seed=page).fill(cuda_lib)
+            verify(b, *attend(cuda_lib, b, 2), 2, 0, 0.11)
+
+
+@pytest.mark.parametrize("rows", [1, 100])
+def test_bad_pages_and_lengths_are_reported(cuda_lib, rows):
+    """A page outside the cache or a length outside the table sets the status; nothing else is touched."""
+    g = cuda_lib
+    for which in ("page", "negative", "long", "short"):
+        b = Batch([rows, rows], [rows + 40, rows + 90], 16, 2, 64, False, seed=1).fill(g)
+        assert g.gdn2_sync_status() == 0
+        q = torch.randn(b.total, 4, 64).bfloat16().cuda()
+        d = b.dev
+        good, _ = g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args())
+        if which == "page":
+            d["table"][1, 0] = b.kc.shape[0]
+        elif which == "negative":
+            d["table"][1, 2] = -1
+        elif which == "long":
+            d["kv"][1] = b.table.shape[1] * 16 + 1
+        else:
+            d["kv"][1] = rows - 1
+        o = torch.full_like(q, 7.0)
+        g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args(), o=o)
+        assert g.gdn2_sync_status() == -11, which
+        assert torch.equal(o[:rows], good[:rows]), which
+        if which in ("long", "short"):
+            assert (o[rows:] == 7.0).all()
+        before = d["kc"].clone()
+        k = torch.randn(b.total, 2, 64).bfloat16().cuda()
+        g.gdn2_cache_write(k, k, d["kc"], d["vc"], d["cu"], d["kv"], d["table"])
+        st = g.gdn2_sync_status()
+        if which in ("long", "short"):
+            assert st == -11
+            # only sequence 0's new rows changed
+            changed = (before.view(torch.int16) != d["kc"].view(torch.int16)).any(-1).any(-1).sum()
+            assert int(changed) == rows
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+def test_repeatable_and_graphs(cuda_lib, e4m3):
+    """Captured and replayed over lengths and pages that changed in place."""
+    g = cuda_lib
+    b = Batch([1, 1, 1], [40, 900, 2500], 16, 2, 128, e4m3, seed=2).fill(g)
+    d = b.dev
+    q = torch.randn(3, 8, 128).bfloat16().cuda()
+    a = g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args())
+    c = g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args())
+    assert all(torch.equal(x, y) for x, y in zip(a, c))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args())
+    d["kv"].copy_(torch.tensor([17, 640, 2100], dtype=torch.int32))
+    want = g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args())
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
