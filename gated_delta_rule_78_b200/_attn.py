@@ -6,7 +6,7 @@ device's current stream, and allocates its outputs and workspace there.
 from __future__ import annotations
 
 import contextlib
-import ctypes
+import math
 
 import torch
 
@@ -17,11 +17,9 @@ ROPE_RMSNORM, ROPE_INTERLEAVED = 1, 2
 # gdn2_cache_type
 CACHE_BF16, CACHE_E4M3 = 0, 1
 
-_NONE = ctypes.c_void_p(None)
-
 
 def _ptr(t):
-    return _NONE if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _bytes(t):
@@ -29,17 +27,16 @@ def _bytes(t):
 
 
 def _need(name, t, dtype, shape, dev):
-    """`t` is a contiguous tensor of this dtype, shape (None: any) and device, or None."""
-    if t is None:
+    """`t` is a contiguous tensor of this dtype, shape (a tuple; None: any) and device, or None."""
+    if t is None or (t.dtype is dtype and t.device == dev and (shape is None or t.shape == shape) and t.is_contiguous()):
         return
-    if t.device != dev or not t.is_cuda:
+    if t.device != dev:
         raise ValueError(f"{name} must be a CUDA tensor on {dev}, is on {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 @contextlib.contextmanager
@@ -51,17 +48,18 @@ def _elsewhere(dev, stream):
 _HERE = contextlib.nullcontext()
 
 
-def _on(t, stream):
+def _on(dev, stream):
     """The device and stream of a call, for its allocations and its launches."""
-    if not t.is_cuda:
-        raise ValueError("q, k, v must be CUDA tensors")
-    if stream is None and t.device.index == torch.cuda.current_device():
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors must be CUDA tensors, are on {dev}")
+    if stream is None and dev.index == torch.cuda.current_device():
         return _HERE
-    return _elsewhere(t.device, torch.cuda.current_stream(t.device) if stream is None else stream)
+    return _elsewhere(dev, torch.cuda.current_stream(dev) if stream is None else stream)
 
 
-def _current():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+def _current(dev):
+    # the handle alone: torch.cuda.current_stream() builds a Stream object, 3 us of a decode step's call
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _workspace(ws, nbytes, dev):
@@ -77,25 +75,24 @@ def _scale(scale, D):
 
 
 # ------------------------------------------------------------------ norm and rotation
-def _rope_args(q, k, q_weight, k_weight, positions, inv_freq, flags):
-    if q.dim() < 2 or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or k.shape[-1] != q.shape[-1]:
+def _rope_args(q, k, q_weight, k_weight, positions, inv_freq):
+    dev, dtype, qs, ks = q.device, q.dtype, q.shape, k.shape
+    if len(qs) < 2 or len(ks) != len(qs) or ks[:-2] != qs[:-2] or ks[-1] != qs[-1]:
         raise ValueError("q and k are [.., H, D] and [.., Hkv, D] over the same rows")
-    dev, H, Hkv, D = q.device, q.shape[-2], k.shape[-2], q.shape[-1]
-    N = q.numel() // (H * D) if H * D else 0
-    _need("q", q, q.dtype, None, dev)
-    _need("k", k, q.dtype, None, dev)
+    H, D = qs[-2:]
+    N = math.prod(qs[:-2])
+    _need("q", q, dtype, qs, dev)
+    _need("k", k, dtype, ks, dev)
     _need("q_weight", q_weight, torch.float32, (D,), dev)
     _need("k_weight", k_weight, torch.float32, (D,), dev)
     rot = 0
     if inv_freq is not None:
         _need("inv_freq", inv_freq, torch.float32, None, dev)
         rot = 2 * inv_freq.numel()
-        if positions is None:
-            raise ValueError("inv_freq needs positions")
+        if positions is None or positions.numel() != N:
+            raise ValueError(f"inv_freq needs positions, one entry for each of the {N} rows")
         _need("positions", positions, torch.int32, None, dev)
-        if positions.numel() != N:
-            raise ValueError(f"positions must hold one entry for each of the {N} rows")
-    return dev, N, H, Hkv, D, rot
+    return dev, dtype, qs, ks, N, H, ks[-2], D, rot
 
 
 def gdn2_qk_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, *, flags=ROPE_RMSNORM, eps=1e-6,
@@ -103,14 +100,18 @@ def gdn2_qk_rope(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=No
     """Per-head RMS norm of q [.., H, D] and k [.., Hkv, D] (with ROPE_RMSNORM) and the rotation of
     their first 2 * len(inv_freq) channels by positions (int32, one per row).  Returns (q_out, k_out);
     q_out may be q and k_out k."""
-    dev, N, H, Hkv, D, rot = _rope_args(q, k, q_weight, k_weight, positions, inv_freq, flags)
-    with _on(q, stream):
-        q_out = torch.empty_like(q) if q_out is None else q_out
-        k_out = torch.empty_like(k) if k_out is None else k_out
-        _need("q_out", q_out, q.dtype, q.shape, dev)
-        _need("k_out", k_out, q.dtype, k.shape, dev)
+    dev, dtype, qs, ks, N, H, Hkv, D, rot = _rope_args(q, k, q_weight, k_weight, positions, inv_freq)
+    with _on(dev, stream):
+        if q_out is None:
+            q_out = torch.empty_like(q)
+        else:
+            _need("q_out", q_out, dtype, qs, dev)
+        if k_out is None:
+            k_out = torch.empty_like(k)
+        else:
+            _need("k_out", k_out, dtype, ks, dev)
         st = raw().gdn2_qk_rope(flags, _dt(q), N, H, Hkv, D, rot, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
-                                _ptr(positions), _ptr(inv_freq), eps, rot_scale, _ptr(q_out), _ptr(k_out), _current())
+                                _ptr(positions), _ptr(inv_freq), eps, rot_scale, _ptr(q_out), _ptr(k_out), _current(dev))
     _check("gdn2_qk_rope", st)
     return q_out, k_out
 
@@ -119,11 +120,11 @@ def gdn2_qk_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, d_q_out, d_k
                      rot_scale=1.0, out=None, workspace=None, stream=None):
     """The gradients of gdn2_qk_rope: dict(dq, dk, dq_weight, dk_weight).  The weight gradients (fp32
     [D]) are None without ROPE_RMSNORM.  Of a given ``out`` a weight gradient may be None."""
-    dev, N, H, Hkv, D, rot = _rope_args(q, k, q_weight, k_weight, positions, inv_freq, flags)
-    _need("d_q_out", d_q_out, q.dtype, q.shape, dev)
-    _need("d_k_out", d_k_out, q.dtype, k.shape, dev)
+    dev, dtype, qs, ks, N, H, Hkv, D, rot = _rope_args(q, k, q_weight, k_weight, positions, inv_freq)
+    _need("d_q_out", d_q_out, dtype, qs, dev)
+    _need("d_k_out", d_k_out, dtype, ks, dev)
     norm = bool(flags & ROPE_RMSNORM)
-    with _on(q, stream):
+    with _on(dev, stream):
         if out is None:
             w = torch.empty(2, D, dtype=torch.float32, device=dev) if norm else (None, None)
             out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dq_weight": w[0], "dk_weight": w[1]}
@@ -137,41 +138,48 @@ def gdn2_qk_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, d_q_out, d_k
         st = raw().gdn2_qk_rope_bwd(flags, _dt(q), N, H, Hkv, D, rot, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
                                     _ptr(positions), _ptr(inv_freq), eps, rot_scale, _ptr(d_q_out), _ptr(d_k_out),
                                     _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dq_weight"]), _ptr(out["dk_weight"]),
-                                    _ptr(workspace), _bytes(workspace), _current())
+                                    _ptr(workspace), _bytes(workspace), _current(dev))
     _check("gdn2_qk_rope_bwd", st)
     return out
 
 
 # ------------------------------------------------------------------ attention over whole sequences
-def _attn_args(q, k, v, packed):
-    rank = 3 if packed else 4
-    if q.dim() != rank or k.dim() != rank:
+def _attn_args(q, k, v, cu_seqlens):
+    dev, dtype, qs, ks = q.device, q.dtype, q.shape, k.shape
+    packed = cu_seqlens is not None
+    if len(qs) != (3 if packed else 4) or len(ks) != len(qs):
         raise ValueError("q and k, v are " + ("[total_T, H, D] and [total_T, Hkv, D]" if packed else
                                               "[B, T, H, D] and [B, T, Hkv, D]"))
-    dev = q.device
-    _need("q", q, q.dtype, None, dev)
-    _need("k", k, q.dtype, q.shape[:-2] + k.shape[-2:-1] + q.shape[-1:], dev)
-    _need("v", v, q.dtype, k.shape, dev)
-    return dev, q.shape[-2], k.shape[-2], q.shape[-1]
+    *lead, H, D = qs
+    _need("q", q, dtype, qs, dev)
+    _need("k", k, dtype, (*lead, ks[-2], D), dev)
+    _need("v", v, dtype, ks, dev)
+    if packed:
+        _need("cu_seqlens", cu_seqlens, torch.int32, None, dev)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens is [N + 1] with N >= 1")
+        lead = (cu_seqlens.numel() - 1, *lead)
+    return dev, dtype, qs, lead, H, ks[-2], D
 
 
 def _attn_fwd(q, k, v, cu_seqlens, window, scale, o, lse, want_lse, stream):
-    packed = cu_seqlens is not None
-    dev, H, Hkv, D = _attn_args(q, k, v, packed)
-    with _on(q, stream):
-        o = torch.empty_like(q) if o is None else o
-        if lse is None and want_lse:
-            lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
-        _need("o", o, q.dtype, q.shape, dev)
-        _need("lse", lse, torch.float32, q.shape[:-1], dev)
-        tail = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _current())
-        if packed:
-            _need("cu_seqlens", cu_seqlens, torch.int32, None, dev)
-            st = raw().gdn2_attn_fwd_varlen(_dt(q), cu_seqlens.numel() - 1, q.shape[0], H, Hkv, D, window,
-                                            _scale(scale, D), _ptr(cu_seqlens), *tail)
+    dev, dtype, qs, (n, t), H, Hkv, D = _attn_args(q, k, v, cu_seqlens)
+    with _on(dev, stream):
+        if o is None:
+            o = torch.empty_like(q)
         else:
-            st = raw().gdn2_attn_fwd(_dt(q), q.shape[0], q.shape[1], H, Hkv, D, window, _scale(scale, D), *tail)
-    _check("gdn2_attn_fwd_varlen" if packed else "gdn2_attn_fwd", st)
+            _need("o", o, dtype, qs, dev)
+        if lse is not None:
+            _need("lse", lse, torch.float32, qs[:-1], dev)
+        elif want_lse:
+            lse = torch.empty(qs[:-1], dtype=torch.float32, device=dev)
+        head = (_dt(q), n, t, H, Hkv, D, window, _scale(scale, D))
+        tail = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _current(dev))
+        if cu_seqlens is not None:
+            st = raw().gdn2_attn_fwd_varlen(*head, _ptr(cu_seqlens), *tail)
+        else:
+            st = raw().gdn2_attn_fwd(*head, *tail)
+    _check("gdn2_attn_fwd" if cu_seqlens is None else "gdn2_attn_fwd_varlen", st)
     return o, lse
 
 
@@ -190,28 +198,26 @@ def gdn2_attn_fwd_varlen(q, k, v, cu_seqlens, *, window=0, scale=None, o=None, l
 
 
 def _attn_bwd(q, k, v, o, lse, d_o, cu_seqlens, window, scale, out, workspace, stream):
-    packed = cu_seqlens is not None
-    dev, H, Hkv, D = _attn_args(q, k, v, packed)
-    _need("o", o, q.dtype, q.shape, dev)
-    _need("d_o", d_o, q.dtype, q.shape, dev)
-    _need("lse", lse, torch.float32, q.shape[:-1], dev)
-    with _on(q, stream):
+    dev, dtype, qs, (n, t), H, Hkv, D = _attn_args(q, k, v, cu_seqlens)
+    _need("o", o, dtype, qs, dev)
+    _need("d_o", d_o, dtype, qs, dev)
+    _need("lse", lse, torch.float32, qs[:-1], dev)
+    with _on(dev, stream):
         if out is None:
             out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v)}
         else:
-            for n, t in (("dq", q), ("dk", k), ("dv", v)):
-                _need(n, out[n], q.dtype, t.shape, dev)
-        N, T = (1, q.shape[0]) if packed else q.shape[:2]
-        workspace = _workspace(workspace, int(raw().gdn2_attn_workspace_size(_dt(q), N, T, H, Hkv, D)), dev)
+            for name, x in (("dq", q), ("dk", k), ("dv", v)):
+                _need(name, out[name], dtype, x.shape, dev)
+        rows = t if cu_seqlens is not None else n * t
+        workspace = _workspace(workspace, int(raw().gdn2_attn_workspace_size(_dt(q), 1, rows, H, Hkv, D)), dev)
+        head = (_dt(q), n, t, H, Hkv, D, window, _scale(scale, D))
         tail = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(d_o), _ptr(out["dq"]), _ptr(out["dk"]),
-                _ptr(out["dv"]), _ptr(workspace), _bytes(workspace), _current())
-        if packed:
-            _need("cu_seqlens", cu_seqlens, torch.int32, None, dev)
-            st = raw().gdn2_attn_bwd_varlen(_dt(q), cu_seqlens.numel() - 1, T, H, Hkv, D, window, _scale(scale, D),
-                                            _ptr(cu_seqlens), *tail)
+                _ptr(out["dv"]), _ptr(workspace), _bytes(workspace), _current(dev))
+        if cu_seqlens is not None:
+            st = raw().gdn2_attn_bwd_varlen(*head, _ptr(cu_seqlens), *tail)
         else:
-            st = raw().gdn2_attn_bwd(_dt(q), N, T, H, Hkv, D, window, _scale(scale, D), *tail)
-    _check("gdn2_attn_bwd_varlen" if packed else "gdn2_attn_bwd", st)
+            st = raw().gdn2_attn_bwd(*head, *tail)
+    _check("gdn2_attn_bwd" if cu_seqlens is None else "gdn2_attn_bwd_varlen", st)
     return out
 
 
@@ -235,29 +241,27 @@ def gdn2_attn_workspace_size(dtype, N: int, T: int, H: int, Hkv: int, D: int) ->
 
 # ------------------------------------------------------------------ the paged cache
 def _cache_args(k_cache, v_cache, cu_seqlens, kv_lens, block_table, k_scale, v_scale):
-    dev = k_cache.device
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache and v_cache are [num_pages, page_size, Hkv, D]")
-    if k_cache.dtype == torch.bfloat16:
+    dev, dtype, shape = k_cache.device, k_cache.dtype, k_cache.shape
+    if len(shape) != 4 or block_table.dim() != 2:
+        raise ValueError("k_cache and v_cache are [num_pages, page_size, Hkv, D], block_table is [N, max_pages]")
+    if dtype is torch.bfloat16:
         kind = CACHE_BF16
-    elif k_cache.dtype == torch.float8_e4m3fn:
+    elif dtype is torch.float8_e4m3fn:
         kind = CACHE_E4M3
         if k_scale is None or v_scale is None:
             raise ValueError("an e4m3 cache has k_scale and v_scale")
-        _need("k_scale", k_scale, torch.float32, k_cache.shape[:3], dev)
-        _need("v_scale", v_scale, torch.float32, k_cache.shape[:3], dev)
+        _need("k_scale", k_scale, torch.float32, shape[:3], dev)
+        _need("v_scale", v_scale, torch.float32, shape[:3], dev)
     else:
-        raise TypeError(f"unsupported cache dtype {k_cache.dtype} (bfloat16 or float8_e4m3fn)")
-    _need("k_cache", k_cache, k_cache.dtype, None, dev)
-    _need("v_cache", v_cache, k_cache.dtype, k_cache.shape, dev)
-    N = kv_lens.numel()
+        raise TypeError(f"unsupported cache dtype {dtype} (bfloat16 or float8_e4m3fn)")
+    pages, page, Hkv, D = shape
+    N, width = block_table.shape
+    _need("k_cache", k_cache, dtype, shape, dev)
+    _need("v_cache", v_cache, dtype, shape, dev)
+    _need("block_table", block_table, torch.int32, (N, width), dev)
     _need("cu_seqlens", cu_seqlens, torch.int32, (N + 1,), dev)
     _need("kv_lens", kv_lens, torch.int32, (N,), dev)
-    if block_table.dim() != 2:
-        raise ValueError("block_table is [N, max_pages]")
-    _need("block_table", block_table, torch.int32, (N, block_table.shape[1]), dev)
-    pages, page, Hkv, D = k_cache.shape
-    return dev, kind, N, Hkv, D, (block_table.shape[1], pages, page)
+    return dev, kind, N, Hkv, D, (width, pages, page)
 
 
 def gdn2_cache_write(k, v, k_cache, v_cache, cu_seqlens, kv_lens, block_table, k_scale=None, v_scale=None, *,
@@ -269,10 +273,10 @@ def gdn2_cache_write(k, v, k_cache, v_cache, cu_seqlens, kv_lens, block_table, k
     T = k.shape[0]
     _need("k", k, torch.bfloat16, (T, Hkv, D), dev)
     _need("v", v, torch.bfloat16, (T, Hkv, D), dev)
-    with _on(k, stream):
+    with _on(dev, stream):
         st = raw().gdn2_cache_write(kind, GDN2_BF16, N, T, Hkv, D, _ptr(cu_seqlens), _ptr(kv_lens), _ptr(block_table),
                                     *sizes, _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                                    _ptr(v_scale), _current())
+                                    _ptr(v_scale), _current(dev))
     _check("gdn2_cache_write", st)
 
 
@@ -285,14 +289,16 @@ def gdn2_cache_read(k_cache, v_cache, cu_seqlens, kv_lens, block_table, k_scale=
         if k is None:
             raise ValueError("give total_T, or k and v")
         total_T = k.shape[0]
-    with _on(k_cache, stream):
-        k = torch.empty(total_T, Hkv, D, dtype=torch.bfloat16, device=dev) if k is None else k
-        v = torch.empty(total_T, Hkv, D, dtype=torch.bfloat16, device=dev) if v is None else v
+    with _on(dev, stream):
+        if k is None:
+            k = torch.empty(total_T, Hkv, D, dtype=torch.bfloat16, device=dev)
+        if v is None:
+            v = torch.empty_like(k)
         _need("k", k, torch.bfloat16, (total_T, Hkv, D), dev)
         _need("v", v, torch.bfloat16, (total_T, Hkv, D), dev)
         st = raw().gdn2_cache_read(kind, GDN2_BF16, N, total_T, Hkv, D, _ptr(cu_seqlens), _ptr(kv_lens),
                                    _ptr(block_table), *sizes, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                                   _ptr(v_scale), _ptr(k), _ptr(v), _current())
+                                   _ptr(v_scale), _ptr(k), _ptr(v), _current(dev))
     _check("gdn2_cache_read", st)
     return k, v
 
@@ -311,18 +317,21 @@ def gdn2_attn_cached(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, k_sc
         raise ValueError("q is [total_T, H, D]")
     T, H = q.shape[:2]
     _need("q", q, torch.bfloat16, (T, H, D), dev)
-    with _on(q, stream):
-        o = torch.empty_like(q) if o is None else o
-        if lse is None and want_lse:
+    with _on(dev, stream):
+        if o is None:
+            o = torch.empty_like(q)
+        else:
+            _need("o", o, torch.bfloat16, (T, H, D), dev)
+        if lse is not None:
+            _need("lse", lse, torch.float32, (T, H), dev)
+        elif want_lse:
             lse = torch.empty(T, H, dtype=torch.float32, device=dev)
-        _need("o", o, torch.bfloat16, q.shape, dev)
-        _need("lse", lse, torch.float32, (T, H), dev)
         if workspace is None:
             workspace = _workspace(None, gdn2_attn_cached_workspace_size(N, T, H, Hkv, D, window, sizes[0], sizes[2]),
                                    dev)
         st = raw().gdn2_attn_cached(kind, GDN2_BF16, N, T, H, Hkv, D, window, _scale(scale, D), _ptr(cu_seqlens),
                                     _ptr(kv_lens), _ptr(block_table), *sizes, _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                     _ptr(k_scale), _ptr(v_scale), _ptr(o), _ptr(lse), _ptr(workspace),
-                                    _bytes(workspace), _current())
+                                    _bytes(workspace), _current(dev))
     _check("gdn2_attn_cached", st)
     return o, lse

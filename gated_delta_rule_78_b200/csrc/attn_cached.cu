@@ -6,9 +6,14 @@
 // r / G, head r % G) and one part of the key axis; its 4 warps take key steps of 16 in turn, each with
 // a ring of its own of cp.async stages, so that no warp waits for another until the end, where their
 // sums are joined in shared memory.  Products are m16n8k16 (16 rows are all there is: a 128-row tile
-// of the fifth-generation tensor core would be 7/8 empty and the time is the loads').  e4m3 rows go
-// to shared memory as they are and become bf16 in registers; a key's scale multiplies its score,
-// a value's scale its weight.
+// of the fifth-generation tensor core would be 7/8 empty and the time is the loads').
+//
+// e4m3 rows go to shared memory as they are and become f16 in registers, one conversion to two values
+// (by way of f32 to bf16 it would be four).  f16 holds every e4m3 value.  Its range asks for care on
+// the other side: a query row is brought below 2^14 by a power of two (exact, but for channels below
+// 2^-28 of the row's largest), and a key's weight p_j scale_j, e4m3's scale of the value with it, is kept
+// below 2^14 by a reference of its own, which like the softmax's follows the largest when that has grown
+// by 2^8: weights are off by 2^-11 of themselves or 2^-31 of the largest.
 //
 // Cut into parts, each part writes its normalised output and log-sum; a second kernel joins them,
 // in a fixed order.
@@ -17,7 +22,6 @@
 namespace gdn2 {
 namespace {
 
-using attn::e4m3x4_bf16;
 using attn::ex2;
 using attn::kLn2;
 using attn::kLog2e;
@@ -25,7 +29,8 @@ using tc::pack_bf16x2;
 using tc::smem_u32;
 
 constexpr int kWarps = 4, kRows = 16, kStep = 16;  // warps, query rows, keys of a warp's step
-constexpr float kGrow = 8.f;  // growth of the maximum (log2) that moves the reference
+constexpr float kGrow = 8.f;    // growth of the maximum (log2) that moves the reference
+constexpr float kWeight = 6.f;  // e4m3: log2 of the weight at the reference
 
 template <int D, bool e4m3> struct Cfg {
     static constexpr int ROW = D * (e4m3 ? 1 : 2);         // bytes of a cache row
@@ -54,6 +59,25 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], 
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Four e4m3 values as two pairs of f16 (exact).
+__device__ __forceinline__ void e4m3x4_f16(uint32_t x, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
 }
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr)
 {
@@ -145,6 +169,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
     // Q fragments: rows g and g + 8.  e4m3 keys come four channels to a lane (see below), so there a
     // lane's k indices 2t, 2t+1, 2t+8, 2t+9 stand for channels 4t .. 4t+3; a sum has no order.
     uint32_t qf[D / 16][4];
+    float qscale[2] = {1.f, 1.f};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int row = g + 8 * i;
@@ -154,6 +179,28 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 qf[k][i + 2 * e] = *reinterpret_cast<const uint32_t *>(q + 16 * k + (e4m3 ? 4 * t + 2 * e : 2 * t + 8 * e));
+        if constexpr (e4m3) {  // f16 of q 2^-x, x from the row's largest finite exponent
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t w = qf[k][i + 2 * e], lo = (w >> 7) & 0xffu, hi = (w >> 23) & 0xffu;
+                    top = max(top, max(lo < 255u ? lo : 0u, hi < 255u ? hi : 0u));
+                }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int x = min(max((int)top - 127 - 13, -120), 120);
+            const float f = __uint_as_float((uint32_t)(127 - x) << 23);
+            qscale[i] = __uint_as_float((uint32_t)(127 + x) << 23);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t w = qf[k][i + 2 * e];
+                    qf[k][i + 2 * e] = pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+                }
+        }
     }
     int pos[2];  // positions of this lane's two rows
 #pragma unroll
@@ -194,7 +241,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < C::ST - 1; ++i) load(i);
 
-    float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // m: reference of the sums l, wm: of the outputs o (the same without a scale of values); log2
+    float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, wm[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int n = 0; n < D / 8; ++n)
 #pragma unroll
@@ -224,37 +272,57 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
                 ldm4(b, sk + chunk<C::ROW>((lane & 7) + (lane & 8), k + (lane >> 4)));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    e4m3x4_bf16(b[e], x, y);
-                    mma_bf16(s[e & 1], qf[k + (e >> 1)], x, y);
+                    e4m3x4_f16(b[e], x, y);
+                    mma_f16(s[e & 1], qf[k + (e >> 1)], x, y);
                 }
             }
         }
         const float *sc = reinterpret_cast<const float *>(ring + (i % C::ST) * C::STAGE + 2 * C::TILE);
         const int k0 = kb + kStep * (warp + kWarps * i) + 2 * t;
-        float top[2] = {m[0], m[1]};
+        // top: the largest score; wtop: the largest log2 weight (e4m3: with the value's scale)
+        float top[2] = {m[0], m[1]}, wtop[2] = {wm[0], wm[1]}, lv[2][2];
+        if constexpr (e4m3) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) lv[n][e] = __log2f(sc[kStep + 8 * n + 2 * t + e]);
+        }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int key = k0 + 8 * n + (e & 1), at = pos[e >> 1];
-                if constexpr (e4m3) s[n][e] *= sc[8 * n + 2 * t + (e & 1)];
-                const bool vis = key <= at && key < ke && (p.window == 0 || key > at - p.window);
+                const int key = k0 + 8 * n + (e & 1), x = e >> 1;
+                if constexpr (e4m3) s[n][e] *= sc[8 * n + 2 * t + (e & 1)] * qscale[x];
+                s[n][e] *= c;
+                const bool vis = key <= pos[x] && key < ke && (p.window == 0 || key > pos[x] - p.window);
                 s[n][e] = vis ? s[n][e] : -INFINITY;
-                top[e >> 1] = fmaxf(top[e >> 1], s[n][e]);
+                top[x] = fmaxf(top[x], s[n][e]);
+                if constexpr (e4m3) wtop[x] = fmaxf(wtop[x], s[n][e] + lv[n][e & 1]);
             }
-        bool grow[2];
+        bool grow[2], wgrow[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
             top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
-            grow[x] = (top[x] - m[x]) * c > kGrow;
+            grow[x] = top[x] - m[x] > kGrow;  // true for the row's first visible key (m = -inf)
+            wgrow[x] = grow[x];
+            if constexpr (e4m3) {
+                wtop[x] = fmaxf(wtop[x], __shfl_xor_sync(0xffffffffu, wtop[x], 1));
+                wtop[x] = fmaxf(wtop[x], __shfl_xor_sync(0xffffffffu, wtop[x], 2));
+                wgrow[x] = wtop[x] - wm[x] > kGrow;
+            } else {
+                wtop[x] = top[x];
+            }
         }
-        if (__any_sync(0xffffffffu, grow[0] || grow[1])) {
+        if (__any_sync(0xffffffffu, grow[0] || grow[1] || wgrow[0] || wgrow[1])) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const float f = grow[x] ? ex2((m[x] - top[x]) * c) : 1.f;
-                if (grow[x]) m[x] = top[x];
-                l[x] *= f;
+                if (grow[x]) {
+                    l[x] *= ex2(m[x] - top[x]);
+                    m[x] = top[x];
+                }
+                const float f = wgrow[x] ? ex2(wm[x] - wtop[x]) : 1.f;
+                if (wgrow[x]) wm[x] = wtop[x];
 #pragma unroll
                 for (int n = 0; n < D / 8; ++n) {
                     o[n][2 * x] *= f;
@@ -262,19 +330,22 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
                 }
             }
         }
-        const float off[2] = {m[0] == -INFINITY ? 0.f : -m[0] * c, m[1] == -INFINITY ? 0.f : -m[1] * c};
         uint32_t pf[4];
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                float a = ex2(fmaf(s[n][2 * x], c, off[x])), b = ex2(fmaf(s[n][2 * x + 1], c, off[x]));
+                const float off = m[x] == -INFINITY ? 0.f : m[x];  // no key visible yet: all weights 0
+                float a = ex2(s[n][2 * x] - off), b = ex2(s[n][2 * x + 1] - off);
                 l[x] += a + b;
                 if constexpr (e4m3) {
-                    a *= sc[kStep + 8 * n + 2 * t];
-                    b *= sc[kStep + 8 * n + 2 * t + 1];
+                    const float woff = wm[x] == -INFINITY ? 0.f : wm[x] - kWeight;
+                    a = ex2(s[n][2 * x] + lv[n][0] - woff);
+                    b = ex2(s[n][2 * x + 1] + lv[n][1] - woff);
+                    pf[x + 2 * n] = pack_f16x2(a, b);
+                } else {
+                    pf[x + 2 * n] = pack_bf16x2(a, b);
                 }
-                pf[x + 2 * n] = pack_bf16x2(a, b);
             }
 #pragma unroll
         for (int d = 0; d < D / 16; d += (e4m3 ? 2 : 1)) {
@@ -290,11 +361,11 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
                 ldm4t(b, sv + chunk<C::ROW>((lane & 7) + (lane & 8), d + (lane >> 4)));
                 uint32_t ev[4], od[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) e4m3x4_bf16(__byte_perm(b[e], 0, 0x3120), ev[e], od[e]);
-                mma_bf16(o[2 * d], pf, ev[0], ev[1]);
-                mma_bf16(o[2 * d + 1], pf, od[0], od[1]);
-                mma_bf16(o[2 * d + 2], pf, ev[2], ev[3]);
-                mma_bf16(o[2 * d + 3], pf, od[2], od[3]);
+                for (int e = 0; e < 4; ++e) e4m3x4_f16(__byte_perm(b[e], 0, 0x3120), ev[e], od[e]);
+                mma_f16(o[2 * d], pf, ev[0], ev[1]);
+                mma_f16(o[2 * d + 1], pf, od[0], od[1]);
+                mma_f16(o[2 * d + 2], pf, ev[2], ev[3]);
+                mma_f16(o[2 * d + 3], pf, od[2], od[3]);
             }
         }
     }
@@ -307,7 +378,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
     // ---- the warps' sums joined: O and (m, l) of each warp over the rings
     __syncthreads();
     float *so = reinterpret_cast<float *>(sm);
-    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+    __shared__ float s_m[kWarps][kRows], s_w[kWarps][kRows], s_l[kWarps][kRows];
     constexpr int OS = D + 4;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -324,6 +395,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
         }
         if (t == 0) {
             s_m[warp][g + 8 * x] = m[x];
+            s_w[warp][g + 8 * x] = e4m3 ? wm[x] - kWeight : m[x];
             s_l[warp][g + 8 * x] = l[x];
         }
     }
@@ -337,16 +409,18 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2((s_m[w][row] - base) * c);
+            // a value's scale can be far from 1, so that 2^(s_w - base) alone may leave fp32's range where
+            // its product with o does not: half of it on either side
+            const float f = ex2(0.5f * (s_w[w][row] - base));
             const float4 v = *reinterpret_cast<const float4 *>(so + (w * kRows + row) * OS + ch);
-            sum += f * s_l[w][row];
-            acc.x += f * v.x;
-            acc.y += f * v.y;
-            acc.z += f * v.z;
-            acc.w += f * v.w;
+            sum += ex2(s_m[w][row] - base) * s_l[w][row];
+            acc.x += f * v.x * f;
+            acc.y += f * v.y * f;
+            acc.z += f * v.z * f;
+            acc.w += f * v.w * f;
         }
         const bool some = sum > 0.f || sum != sum;
-        const float inv = some ? 1.f / sum : 0.f, lse = some ? (top * c + __log2f(sum)) * kLn2 : -INFINITY;
+        const float inv = some ? 1.f / sum : 0.f, lse = some ? (top + __log2f(sum)) * kLn2 : -INFINITY;
         acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         const size_t at = row_at(row);
         if (p.splits > 1) {
@@ -359,12 +433,15 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
     }
 }
 
-// o = sum_z 2^(lse_z - top) o_z / sum_z 2^(lse_z - top): a warp to a (token, head) row.  Rows of no
-// sequence, or of one that was skipped, are left as they are.
-template <int D> __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ Params p)
+// o = sum_z e^(lse_z - top) o_z / sum_z e^(lse_z - top) over the parts z, in a fixed order.  A warp
+// to a (token, head) row, or a block of 8 warps where there are many parts (few rows, then: the warps
+// take every 8th part).  Rows of no sequence, or of one that was skipped, are left as they are.
+template <int D, int W> __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ Params p)
 {
-    const long long at = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    constexpr int E = D / 32, kAhead = 4;
+    __shared__ float s_top[8], s_sum[8], s_acc[W > 1 ? 8 : 1][D];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = W > 1 ? warp : 0;
+    const long long at = W > 1 ? blockIdx.x : (long long)blockIdx.x * 8 + warp;
     const long long n = p.b.rows * p.H;
     if (at >= n) return;
     SeqSpan sp;
@@ -372,36 +449,65 @@ template <int D> __global__ void __launch_bounds__(256) attn_join_kernel(const _
     if (seq < 0) return;
     const int kvlen = p.c.kv_lens[seq];
     if (kvlen < sp.len || kvlen > (long long)p.c.width * p.c.page) return;
-    constexpr int E = D / 32;
     float acc[E] = {}, top = -INFINITY, sum = 0.f;
-    for (int z = lane; z < p.splits; z += 32) top = fmaxf(top, p.part_l[(size_t)z * n + at]);
+    for (int z0 = w; z0 < p.splits; z0 += 32 * W) {
+        const int zl = z0 + W * lane;
+        const float mine = zl < p.splits ? p.part_l[(size_t)zl * n + at] : -INFINITY;
+        float t = mine;
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    for (int z0 = 0; z0 < p.splits; z0 += 32) {
-        const float mine = z0 + lane < p.splits ? p.part_l[(size_t)(z0 + lane) * n + at] : -INFINITY;
-        const float wt = mine == -INFINITY ? 0.f : ex2((mine - top) * kLog2e);  // NaN stays NaN
-        unsigned some = __ballot_sync(0xffffffffu, mine != -INFINITY);
-        sum += wt;
-        while (some) {
-            const int z = __ffs(some) - 1;
-            some &= some - 1;
-            const float f = __shfl_sync(0xffffffffu, wt, z);
-            const float *src = p.part_o + ((size_t)(z0 + z) * n + at) * D + lane * E;
-            if constexpr (E == 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(src);
-                acc[0] += f * v.x;
-                acc[1] += f * v.y;
-                acc[2] += f * v.z;
-                acc[3] += f * v.w;
-            } else {
-                const float2 v = *reinterpret_cast<const float2 *>(src);
-                acc[0] += f * v.x;
-                acc[1] += f * v.y;
+        for (int m = 16; m >= 1; m >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, m));
+        t = fmaxf(t, top);
+        const float old = top == -INFINITY ? 0.f : ex2((top - t) * kLog2e);
+        const float wt = mine == -INFINITY ? 0.f : ex2((mine - t) * kLog2e);  // NaN stays NaN
+        top = t;
+        sum = sum * old + wt;  // lane by lane, summed at the end
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= old;
+        const int cnt = min(32, (p.splits - z0 + W - 1) / W);
+        for (int z = 0; z < cnt; z += kAhead) {
+            float v[kAhead][E], f[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                f[i] = __shfl_sync(0xffffffffu, wt, (z + i) & 31);
+                if (z + i >= cnt) f[i] = 0.f;
+                const float *src = p.part_o + ((size_t)(z0 + W * (z + i)) * n + at) * D + lane * E;
+#pragma unroll
+                for (int e = 0; e < E; e += 2) {  // an empty part has written no output
+                    const float2 x = f[i] != 0.f ? *reinterpret_cast<const float2 *>(src + e) : make_float2(0.f, 0.f);
+                    v[i][e] = x.x;
+                    v[i][e + 1] = x.y;
+                }
             }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] += f[i] * v[i][e];
         }
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if constexpr (W > 1) {
+        if (lane == 0) {
+            s_top[warp] = top;
+            s_sum[warp] = sum;
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+        __syncthreads();
+        if (warp > 0) return;
+#pragma unroll
+        for (int i = 0; i < W; ++i) top = fmaxf(top, s_top[i]);
+        sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const float f = s_top[i] == -INFINITY ? 0.f : ex2((s_top[i] - top) * kLog2e);
+            sum += f * s_sum[i];
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += f * s_acc[i][lane * E + e];
+        }
+    }
     const bool any = sum > 0.f || sum != sum;
     const float inv = any ? 1.f / sum : 0.f;
     __nv_bfloat16 *dst = p.o + at * D + lane * E;
@@ -482,8 +588,9 @@ cudaError_t launch_attn_cached(const CachedArgs &a, bool use_tc, cudaStream_t s)
         else e = a.D == 128 ? run<128, false>(p, grid, s) : run<64, false>(p, grid, s);
     }
     if (e != cudaSuccess || a.splits == 1) return e;
-    const unsigned blocks = (unsigned)((a.b.rows * a.H + 7) / 8);
-    (a.D == 128 ? attn_join_kernel<128> : attn_join_kernel<64>)<<<blocks, 256, 0, s>>>(p);
+    const long long rows = a.b.rows * a.H;
+    if (a.splits > 8) (a.D == 128 ? attn_join_kernel<128, 8> : attn_join_kernel<64, 8>)<<<(unsigned)rows, 256, 0, s>>>(p);
+    else (a.D == 128 ? attn_join_kernel<128, 1> : attn_join_kernel<64, 1>)<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
     return cudaGetLastError();
 }
 

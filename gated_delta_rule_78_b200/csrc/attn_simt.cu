@@ -164,19 +164,23 @@ template <int D> __global__ void __launch_bounds__(kThreads) attn_fwd_kernel(con
     }
 }
 
-// delta[row, h] = sum over channels of d_o * o; one warp to a (row, head)
+// delta[row, h] = sum over channels of d_o * o; 16 bytes a lane, as many lanes to a (row, head) as it
+// has of them, both loads in flight at once.  Bound by memory.
 template <typename T, int D> __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnArgs a)
 {
-    const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= a.b.rows * a.H) return;
-    const T *x = (const T *)a.o + row * D, *y = (const T *)a.d_o + row * D;
+    constexpr int V = 16 / sizeof(T), L = D / V;
+    const long long n = a.b.rows * a.H, i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long row = i / L;
     float sum = 0.f;
+    if (row < n) {
+        const uint4 x = reinterpret_cast<const uint4 *>(a.o)[i], y = reinterpret_cast<const uint4 *>(a.d_o)[i];
+        const T *xs = reinterpret_cast<const T *>(&x), *ys = reinterpret_cast<const T *>(&y);
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) sum += to_f<T>(x[lane * (D / 32) + c]) * to_f<T>(y[lane * (D / 32) + c]);
+        for (int e = 0; e < V; ++e) sum += to_f<T>(xs[e]) * to_f<T>(ys[e]);
+    }
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    if (lane == 0) a.delta[row] = sum;
+    for (int m = L / 2; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (row < n && threadIdx.x % L == 0) a.delta[row] = sum;
 }
 
 // p and ds of one tile, from the scores s and the products dp = do . v, into P and S
@@ -307,7 +311,8 @@ cudaError_t launch_attn_fwd_simt(const AttnArgs &a, cudaStream_t s)
 
 cudaError_t launch_attn_delta(bool fp32, const AttnArgs &a, cudaStream_t s)
 {
-    const unsigned grid = (unsigned)((a.b.rows * a.H + 7) / 8);
+    const long long lanes = a.b.rows * a.H * (a.D * (fp32 ? 4 : 2) / 16);
+    const unsigned grid = (unsigned)((lanes + 255) / 256);
     if (fp32) (a.D == 128 ? attn_delta_kernel<float, 128> : attn_delta_kernel<float, 64>)<<<grid, 256, 0, s>>>(a);
     else (a.D == 128 ? attn_delta_kernel<__nv_bfloat16, 128> : attn_delta_kernel<__nv_bfloat16, 64>)<<<grid, 256, 0, s>>>(a);
     return cudaGetLastError();

@@ -19,19 +19,22 @@ namespace gdn2 {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kShareBelow = 2048;  // tokens
 
 template <typename T> struct Vec;
 template <> struct Vec<float> { static constexpr int n = 4; };
 template <> struct Vec<__nv_bfloat16> { static constexpr int n = 8; };
 
-__device__ __forceinline__ void load_vec(const float *p, float (&f)[4])
+template <typename T> __device__ __forceinline__ uint4 load_raw(const T *p) { return *reinterpret_cast<const uint4 *>(p); }
+__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[4])
 {
-    const float4 v = *reinterpret_cast<const float4 *>(p);
-    f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
 }
-__device__ __forceinline__ void load_vec(const __nv_bfloat16 *p, float (&f)[8])
+__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[8])
 {
-    const uint4 v = *reinterpret_cast<const uint4 *>(p);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -69,7 +72,8 @@ __device__ __forceinline__ void angle(int pos, float inv, float f, float &c, flo
 // that ends inside a vector, exchanged through shared memory.
 enum { kPair, kSwap, kAny };
 
-// Rotates this lane's vector f (channels ch .. ch + V - 1 of its row) in place; dir = -1 transposes.
+// Rotates this lane's vector f (channels ch .. ch + V - 1 of its row) in place; the backward's
+// transpose comes as negated sines.
 template <int V, int mode>
 __device__ __forceinline__ void rotate(float (&f)[V], const float (&c)[V], const float (&s)[V], int ch, int rot,
                                        float *buf, int lane)
@@ -78,12 +82,11 @@ __device__ __forceinline__ void rotate(float (&f)[V], const float (&c)[V], const
 #pragma unroll
         for (int e = 0; e < V; e += 2) {
             const float a = f[e], b = f[e + 1];
-            if (ch + e < rot) {
-                f[e] = a * c[e] - b * s[e];
-                f[e + 1] = b * c[e] + a * s[e];
-            }
+            f[e] = a * c[e] - b * s[e];
+            f[e + 1] = b * c[e] + a * s[e];
         }
     } else {
+        // c = 1, s = 0 past rot; s is negative in the lower half
         const int half = rot >> 1;
         float o[V];
         if constexpr (mode == kSwap) {
@@ -104,11 +107,7 @@ __device__ __forceinline__ void rotate(float (&f)[V], const float (&c)[V], const
             }
         }
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const int i = ch + e;
-            if (i < half) f[e] = f[e] * c[e] - o[e] * s[e];
-            else if (i < rot) f[e] = f[e] * c[e] + o[e] * s[e];
-        }
+        for (int e = 0; e < V; ++e) f[e] = f[e] * c[e] + (s[e] != 0.f ? o[e] * s[e] : 0.f);
     }
 }
 
@@ -116,10 +115,12 @@ template <typename T, int D, int mode, bool bwd>
 __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeArgs a)
 {
     constexpr int V = Vec<T>::n, L = D / V, R = 32 / L;  // elements per lane, lanes per row, rows per warp pass
+    constexpr int U = bwd ? 2 : 4;                       // passes whose loads are in flight together
     __shared__ float sbuf[mode == kAny ? kWarps * R * D : 1];
+    __shared__ float2 scs[kWarps][D / 2];
     __shared__ float sw[bwd ? kWarps * R : 1][bwd ? D : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int ch = (lane % L) * V, sub = lane / L;
+    const int ch = (lane % L) * V, sub = lane / L, half = a.rot >> 1;
     float *buf = sbuf + (mode == kAny ? (warp * R + sub) * D : 0);
     float wt[2][V], dw[2][V];
 #pragma unroll
@@ -130,96 +131,98 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeArgs a)
     }
     // Few tokens: the warps of a block share one token's heads (a decode step then fills the SMs);
     // many: a warp to a token, whose angles are formed once.
-    const int share = a.n < 2048 ? kWarps : 1;
+    const int share = a.n < kShareBelow ? kWarps : 1, heads = a.H + a.Hkv;
+    const int first = share == 1 ? 0 : warp * R, step = share == 1 ? R : kWarps * R;
     const long long per = kWarps / share;
     for (long long t0 = (long long)blockIdx.x * per; t0 < a.n; t0 += (long long)gridDim.x * per) {
         const long long t = t0 + (share == 1 ? warp : 0);
         if (t >= a.n) break;
-        float c[V], s[V];
-        {
-            const int pos = a.rot ? a.pos[t] : 0, half = a.rot >> 1;
-            if constexpr (mode == kPair) {
+        const int pos = a.rot ? a.pos[t] : 0;
+        uint4 xr[U], gr[U];  // vectors of the next U passes, as loaded
+        auto fetch = [&](int h0) {
 #pragma unroll
-                for (int e = 0; e < V; e += 2) {
-                    c[e] = 1.f;
-                    s[e] = 0.f;
-                    if (ch + e < a.rot) angle(pos, a.inv[(ch + e) >> 1], a.rot_scale, c[e], s[e]);
-                    if (bwd) s[e] = -s[e];
-                }
-            } else if constexpr (mode == kSwap) {
-                // both halves use the same angles: the lower half's lanes form them
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    c[e] = 1.f;
-                    s[e] = 0.f;
-                    if (ch < half) angle(pos, a.inv[ch + e], a.rot_scale, c[e], s[e]);
-                }
-                const int src = ch >= half && ch < a.rot ? lane - half / V : lane;
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    c[e] = __shfl_sync(0xffffffffu, c[e], src);
-                    s[e] = __shfl_sync(0xffffffffu, s[e], src);
-                    if (bwd) s[e] = -s[e];
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const int i = ch + e;
-                    c[e] = 1.f;
-                    s[e] = 0.f;
-                    if (i < a.rot) angle(pos, a.inv[i < half ? i : i - half], a.rot_scale, c[e], s[e]);
-                    if (bwd) s[e] = -s[e];
-                }
+            for (int u = 0; u < U; ++u) {
+                const int h = h0 + u * step + sub;
+                xr[u] = gr[u] = make_uint4(0, 0, 0, 0);
+                if (h >= heads) continue;
+                const bool isk = h >= a.H;
+                const size_t off = ((size_t)t * (isk ? a.Hkv : a.H) + (isk ? h - a.H : h)) * D + ch;
+                if (!bwd || a.norm) xr[u] = load_raw(static_cast<const T *>(isk ? a.k : a.q) + off);
+                if (bwd) gr[u] = load_raw(static_cast<const T *>(isk ? a.dko : a.dqo) + off);
             }
+        };
+        fetch(first);
+        // the token's angles, two or one to a lane
+        __syncwarp();
+        for (int i = lane; i < half; i += 32) {
+            float c, s;
+            angle(pos, a.inv[i], a.rot_scale, c, s);
+            scs[warp][i] = make_float2(c, bwd ? -s : s);
         }
-        const int heads = a.H + a.Hkv;
-        const int first = share == 1 ? 0 : warp * R, step = share == 1 ? R : kWarps * R;
-        for (int h0 = first; h0 < heads; h0 += step) {
-            const int h = h0 + sub;
-            const bool live = h < heads, isk = h >= a.H;
-            const int hh = live ? (isk ? h - a.H : h) : 0;
-            const size_t off = ((size_t)t * (isk ? a.Hkv : a.H) + hh) * D + ch;
-            float x[V], g[V];
+        __syncwarp();
+        float c[V], s[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) x[e] = g[e] = 0.f;
-            if (live && (!bwd || a.norm)) load_vec(static_cast<const T *>(isk ? a.k : a.q) + off, x);
-            if (bwd && live) load_vec(static_cast<const T *>(isk ? a.dko : a.dqo) + off, g);
-            float r = 1.f;
-            if (a.norm) {
-                float ss = 0.f;
+        for (int e = 0; e < V; ++e) {
+            const int i = ch + e;
+            const int at = mode == kPair ? i >> 1 : i < half ? i : i - half;
+            const float2 cs = i < a.rot ? scs[warp][at] : make_float2(1.f, 0.f);
+            c[e] = cs.x;
+            s[e] = mode != kPair && i < half ? -cs.y : cs.y;
+        }
+        for (int h0 = first; h0 < heads; h0 += U * step) {
+            uint4 xn[U], gn[U];
 #pragma unroll
-                for (int e = 0; e < V; ++e) ss += x[e] * x[e];
-#pragma unroll
-                for (int m = L / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-                r = rsqrtf(ss * (1.f / D) + a.eps);
+            for (int u = 0; u < U; ++u) {
+                xn[u] = xr[u];
+                gn[u] = gr[u];
             }
-            if constexpr (!bwd) {
-                if (a.norm) {
+            if (h0 + U * step < heads) fetch(h0 + U * step);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) x[e] = x[e] * r * (isk ? wt[1][e] : wt[0][e]);
+            for (int u = 0; u < U; ++u) {
+                const int h = h0 + u * step + sub;
+                if (h0 + u * step >= heads) break;  // the whole warp's pass
+                const bool live = h < heads, isk = h >= a.H;
+                const size_t off = ((size_t)t * (isk ? a.Hkv : a.H) + (live ? (isk ? h - a.H : h) : 0)) * D + ch;
+                float x[V], g[V];
+                unpack(xn[u], x);
+                if (bwd) unpack(gn[u], g);
+                float r = 1.f;
+                if (a.norm) {
+                    float ss = 0.f;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) ss += x[e] * x[e];
+#pragma unroll
+                    for (int m = L / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+                    r = rsqrtf(ss * (1.f / D) + a.eps);
                 }
-                rotate<V, mode>(x, c, s, ch, a.rot, buf, lane);
-                if (live) store_vec(static_cast<T *>(isk ? a.ko : a.qo) + off, x);
-            } else {
-                rotate<V, mode>(g, c, s, ch, a.rot, buf, lane);
-                if (a.norm) {
-                    float dot = 0.f;
+                if constexpr (!bwd) {
+                    if (a.norm) {
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        x[e] *= r;  // the normalised row
-                        const float ux = g[e] * x[e];
-                        dw[0][e] += isk ? 0.f : ux;
-                        dw[1][e] += isk ? ux : 0.f;
-                        g[e] *= isk ? wt[1][e] : wt[0][e];
-                        dot += g[e] * x[e];
+                        for (int e = 0; e < V; ++e) x[e] = x[e] * r * (isk ? wt[1][e] : wt[0][e]);
                     }
+                    rotate<V, mode>(x, c, s, ch, a.rot, buf, lane);
+                    if (live) store_vec(static_cast<T *>(isk ? a.ko : a.qo) + off, x);
+                } else {
+                    rotate<V, mode>(g, c, s, ch, a.rot, buf, lane);
+                    if (a.norm) {
+                        float dot = 0.f;
 #pragma unroll
-                    for (int m = L / 2; m >= 1; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-                    dot *= 1.f / D;
+                        for (int e = 0; e < V; ++e) {
+                            x[e] *= r;  // the normalised row
+                            const float ux = g[e] * x[e];
+                            dw[0][e] += isk ? 0.f : ux;
+                            dw[1][e] += isk ? ux : 0.f;
+                            g[e] *= isk ? wt[1][e] : wt[0][e];
+                            dot += g[e] * x[e];
+                        }
 #pragma unroll
-                    for (int e = 0; e < V; ++e) g[e] = r * (g[e] - x[e] * dot);
+                        for (int m = L / 2; m >= 1; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+                        dot *= 1.f / D;
+#pragma unroll
+                        for (int e = 0; e < V; ++e) g[e] = r * (g[e] - x[e] * dot);
+                    }
+                    if (live) store_vec(static_cast<T *>(isk ? a.dk : a.dq) + off, g);
                 }
-                if (live) store_vec(static_cast<T *>(isk ? a.dk : a.dq) + off, g);
             }
         }
     }
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float *partial, int
 
 unsigned rope_grid(long long n)
 {
-    const long long want = n < 2048 ? n : (n + kWarps - 1) / kWarps;
+    const long long want = n < kShareBelow ? n : (n + kWarps - 1) / kWarps;
     const long long most = (long long)device_sms() * 4;
     return (unsigned)(want < most ? want : most);
 }
@@ -278,8 +281,11 @@ template <typename T, int D, bool bwd> void run(const RopeArgs &a, unsigned grid
 
 int device_sms()
 {
-    int dev = 0, sms = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    static const int sms = [] {  // of the first device asked: every B200 has as many
+        int dev = 0, n = 148;
+        if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        return n > 0 ? n : 148;
+    }();
     return sms;
 }
 
