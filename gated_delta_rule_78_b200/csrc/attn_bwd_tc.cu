@@ -60,13 +60,6 @@ __device__ __forceinline__ void st64(uint32_t t, const float (&s)[64])
     tmem_st32(t, w);
     tmem_wait_st();
 }
-// D (128 x kN) (+)= A B, A = 128 x 128 bf16 left by st64 of both column halves (64 columns apart)
-template <int D> __device__ __forceinline__ void mma_grad(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc)
-{
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
-        mma_ts(d, a + 64 * (ks >> 2) + 8 * (ks & 3), sdesc_sw128(b + ks * 2048, kBoxBytes, 1024), idesc, acc || ks > 0);
-}
 // f * (this thread's row of TMEM columns [0, n)) as bf16 at dst
 template <int n> __device__ __forceinline__ void store_row(uint32_t t, float f, __nv_bfloat16 *dst, bool live)
 {
@@ -86,16 +79,7 @@ template <int n> __device__ __forceinline__ void store_row(uint32_t t, float f, 
         }
     }
 }
-// after a wait that gave up: products in flight end before the block frees its memory
-__device__ __forceinline__ void drain(uint64_t *bar)
-{
-    if ((threadIdx.x & 31) == 0) {
-        mma_commit(bar);
-        mbar_wait(bar, 0, 1000000000ull);
-    }
-    __syncwarp();
-}
-// ... and so do the loads of a ring, `n` of them issued
+// after a wait that gave up: the loads of a ring, `n` of them issued, end before the block's memory is free
 __device__ __forceinline__ void drain_ring(uint64_t *full, int n, int stages)
 {
     for (int i = n > stages ? n - stages : 0; i < n; ++i) mbar_wait(&full[i % stages], (i / stages) & 1, 1000000000ull);
@@ -123,10 +107,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
         ds_ready, done, bar_drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) report_bad_seqlens(p.b, p.status);
     TileRef r;
     if (!find_tile(p.b, gridDim.x - 1 - blockIdx.x, p.TQ, r)) return;
+    r.tile = uniform(r.tile);
+    r.sp.len = uniform(r.sp.len);
     const int hk = blockIdx.y, len = r.sp.len, t0 = r.tile * p.TQ, nt = min(p.TQ, len - t0);
     const int jb = p.window == 0 || t0 < p.window ? 0 : (t0 - p.window + 1) / kBN, n = (t0 + nt - 1) / kBN + 1 - jb;
 
@@ -156,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = uniform(s_tmem);
 
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -206,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
         const uint32_t bq = smem_u32(sq), bo = smem_u32(so), bk = smem_u32(sk), bv = smem_u32(sv);
         constexpr uint32_t kS = idesc_bf16(128, kBN, 0, 0), kG = idesc_bf16(128, D, 0, 1);
         if (warp == 8) {
+            const uint32_t leader = elect();
             bool ok = wait_warp(&bar_q, 0, &s_abort, p.status);
             auto scores = [&](int it) {
                 const int st = it % C::KS;
@@ -213,37 +200,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
                 // keys past the sequence are another's: their ds is 0, but 0 * NaN is not
                 if ((jb + it + 1) * kBN > len) zero_rows<C::NB>(sk + st * C::TILE, len - (jb + it) * kBN);
                 tc_fence_after();
-                if (lane == 0) {
-                    mma_kk<D / 16, kBM, kBN>(tmem + 128 * (it & 1), bq, bk + st * C::TILE, kS, false);
-                    mma_commit(&s_full[it & 1]);
-                }
+                mma_kk<D / 16>(leader, tmem + 128 * (it & 1), bq, bk + st * C::TILE, kS);
+                commit(leader, &s_full[it & 1]);
                 return true;
             };
             auto products = [&](int it) {
                 const int st = it % C::VS;
                 if (!wait_warp(&v_full[st], (it / C::VS) & 1, &s_abort, p.status)) return false;
                 tc_fence_after();
-                if (lane == 0) {
-                    mma_kk<D / 16, kBM, kBN>(tmem + kTmP, bo, bv + st * C::TILE, kS, false);
-                    mma_commit(&p_full);
-                    mma_commit(&v_empty[st]);
-                }
+                mma_kk<D / 16>(leader, tmem + kTmP, bo, bv + st * C::TILE, kS);
+                commit(leader, &p_full);
+                commit(leader, &v_empty[st]);
                 return true;
             };
             if (ok) ok = scores(0) && products(0) && (n < 2 || scores(1));
             for (int it = 0; ok && it < n; ++it) {
                 if (!(ok = wait_warp(&ds_ready, it & 1, &s_abort, p.status))) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    mma_grad<D>(tmem + kTmQ, tmem + 128 * (it & 1), bk + (it % C::KS) * C::TILE, kG, it > 0);
-                    mma_commit(&k_empty[it % C::KS]);
-                    if (it + 1 == n) mma_commit(&done);
-                }
-                __syncwarp();
+                mma_tn<64>(leader, tmem + kTmQ, tmem + 128 * (it & 1), bk + (it % C::KS) * C::TILE, kG, it > 0);
+                commit(leader, &k_empty[it % C::KS]);
+                if (it + 1 == n) commit(leader, &done);
                 if (it + 1 < n) ok = products(it + 1);
                 if (ok && it + 2 < n) ok = scores(it + 2);
             }
-            if (s_abort) drain(&bar_drain);
+            if (s_abort) drain(leader, &bar_drain);
         } else if (warp == 9 && lane == 0) {
             mbar_expect_tx(&bar_q, 2 * C::NB * 128 * p.G * p.TQ);
             load_tile<C::NB>(sq, &maps.q, hk * p.G, r.sp.bos + t0, &bar_q);
@@ -300,9 +280,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
         p_full, p_ready, ds_ready, done, bar_drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     TileRef r;
     if (!find_tile(p.b, blockIdx.x, kBN, r)) return;
+    r.tile = uniform(r.tile);
+    r.sp.len = uniform(r.sp.len);
     const int hk = blockIdx.y, len = r.sp.len, k0 = r.tile * kBN;
     // query tokens that see a key of this tile: k0 .. end - 1, in tiles of TQ from the sequence's start
     const int end = p.window == 0 || p.window > len ? len : min(len, k0 + kBN - 1 + p.window);
@@ -334,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = uniform(s_tmem);
 
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -385,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
         const uint32_t bq = smem_u32(sq), bo = smem_u32(so), bk = smem_u32(sk), bv = smem_u32(sv);
         constexpr uint32_t kS = idesc_bf16(128, kBM, 0, 0), kG = idesc_bf16(128, D, 0, 1);
         if (warp == 8) {
+            const uint32_t leader = elect();
             bool ok = wait_warp(&bar_kv, 0, &s_abort, p.status);
             // the tile's rows past its tokens (another sequence's, or never loaded) become zeros: their p and
             // ds are 0, but 0 * NaN is not
@@ -393,10 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
                 if (!wait_warp(&q_full[st], (it / C::ST) & 1, &s_abort, p.status)) return false;
                 if (rows < kBM) zero_rows<C::NB>(sq + st * C::TILE, rows);
                 tc_fence_after();
-                if (lane == 0) {
-                    mma_kk<D / 16, kBN, kBM>(tmem, bk, bq + st * C::TILE, kS, false);
-                    mma_commit(&s_full);
-                }
+                mma_kk<D / 16>(leader, tmem, bk, bq + st * C::TILE, kS);
+                commit(leader, &s_full);
                 return true;
             };
             auto products = [&](int it) {
@@ -404,10 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
                 if (!wait_warp(&o_full[st], (it / C::ST) & 1, &s_abort, p.status)) return false;
                 if (rows < kBM) zero_rows<C::NB>(so + st * C::TILE, rows);
                 tc_fence_after();
-                if (lane == 0) {
-                    mma_kk<D / 16, kBN, kBM>(tmem + kTmP, bv, bo + st * C::TILE, kS, false);
-                    mma_commit(&p_full);
-                }
+                mma_kk<D / 16>(leader, tmem + kTmP, bv, bo + st * C::TILE, kS);
+                commit(leader, &p_full);
                 return true;
             };
             if (ok) ok = scores(0) && products(0);
@@ -415,23 +394,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
                 const int st = it % C::ST;
                 if (!(ok = wait_warp(&p_ready, it & 1, &s_abort, p.status))) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    mma_grad<D>(tmem + kTmV, tmem, bo + st * C::TILE, kG, it > 0);
-                    mma_commit(&o_empty[st]);
-                }
-                __syncwarp();
+                mma_tn<64>(leader, tmem + kTmV, tmem, bo + st * C::TILE, kG, it > 0);
+                commit(leader, &o_empty[st]);
                 if (it + 1 < n && !(ok = scores(it + 1))) break;
                 if (!(ok = wait_warp(&ds_ready, it & 1, &s_abort, p.status))) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    mma_grad<D>(tmem + kTmK, tmem + kTmP, bq + st * C::TILE, kG, it > 0);
-                    mma_commit(&q_empty[st]);
-                    if (it + 1 == n) mma_commit(&done);
-                }
-                __syncwarp();
+                mma_tn<64>(leader, tmem + kTmK, tmem + kTmP, bq + st * C::TILE, kG, it > 0);
+                commit(leader, &q_empty[st]);
+                if (it + 1 == n) commit(leader, &done);
                 if (it + 1 < n) ok = products(it + 1);
             }
-            if (s_abort) drain(&bar_drain);
+            if (s_abort) drain(leader, &bar_drain);
         } else if (warp == 9 && lane == 0) {
             mbar_expect_tx(&bar_kv, 2 * C::TILE);
             load_tile<C::NB>(sk, &maps.k, hk, r.sp.bos + k0, &bar_kv);

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kind != kWhole ? 512 : 384, 1) attn_fwd_tc_ker
     __shared__ uint32_t s_tmem;
     __shared__ float s_ks[e4m3 ? SS : 1][kBN], s_vs[e4m3 ? SS : 1][kBN];
     __shared__ volatile int s_abort;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 0) report_bad_seqlens(p.b, p.status);
     TileRef r;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kind != kWhole ? 512 : 384, 1) attn_fwd_tc_ker
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = uniform(s_tmem);
 
     if (warp < 8) {  // ---- softmax of tile A (warps 0-3) or B (4-7): thread = row
         if constexpr (paged) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
@@ -313,51 +313,44 @@ __global__ void __launch_bounds__(kind != kWhole ? 512 : 384, 1) attn_fwd_tc_ker
         if (warp == 8) {  // ---- the products
             constexpr uint32_t kS = idesc_bf16(128, kBN, 0, 0), kO = idesc_bf16(128, D, 0, 1);
             bool ok = g.je > g.jb && wait_warp(&bar_q, 0, &s_abort, p.status);
+            const uint32_t leader = elect();
             uint32_t ph[2] = {0, 0};
-            for (int j = g.jb - 1; ok && j < g.je; ++j) {
-                const int it = j - g.jb, nx = it + 1;  // key tile j and the next one in the rings
+            const int jb = uniform(g.jb), je = uniform(g.je), kvlen = uniform(g.kvlen);
+            const int beg[2] = {uniform(g.beg[0]), uniform(g.beg[1])}, end[2] = {uniform(g.end[0]), uniform(g.end[1])};
+            for (int j = jb - 1; ok && j < je; ++j) {
+                const int it = j - jb, nx = it + 1;  // key tile j and the next one in the rings
                 bool have_v = false, have_k = false;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    if (j >= g.beg[x] && j < g.end[x]) {
+                    if (j >= beg[x] && j < end[x]) {
                         if (!have_v) {
                             if (!(ok = wait_warp(&v_full[it % C::ST], (it / C::ST) & 1, &s_abort, p.status))) break;
                             // rows past the sequence hold other sequences' values: 0 * NaN is not 0
-                            if (!paged && (j + 1) * kBN > g.kvlen) zero_rows<C::NB>(sv + (it % C::ST) * C::TILE, g.kvlen - j * kBN);
+                            if (!paged && (j + 1) * kBN > kvlen) zero_rows<C::NB>(sv + (it % C::ST) * C::TILE, kvlen - j * kBN);
                             have_v = true;
                         }
                         if (!(ok = wait_warp(&p_ready[x], ph[x], &s_abort, p.status))) break;
                         ph[x] ^= 1;
                         tc_fence_after();
-                        if (lane == 0)
-                            mma_tn<8, kBN>(tmem + kTmO + D * x, tmem + kTmS + 128 * x, bv + (it % C::ST) * C::TILE, kO, j > g.beg[x]);
-                        if (lane == 0 && j + 1 == g.end[x]) mma_commit(&o_done[x]);
+                        mma_tn<32>(leader, tmem + kTmO + D * x, tmem + kTmS + 128 * x, bv + (it % C::ST) * C::TILE, kO, j > beg[x]);
+                        if (j + 1 == end[x]) commit(leader, &o_done[x]);
                     }
-                    if (j + 1 >= g.beg[x] && j + 1 < g.end[x]) {
+                    if (j + 1 >= beg[x] && j + 1 < end[x]) {
                         if (!have_k) {
                             if (!(ok = wait_warp(&k_full[nx % C::ST], (nx / C::ST) & 1, &s_abort, p.status))) break;
                             have_k = true;
                         }
                         tc_fence_after();
-                        if (lane == 0) {
-                            mma_kk<D / 16, kBM, kBN>(tmem + kTmS + 128 * x, bq + x * C::TILE, bk + (nx % C::ST) * C::TILE, kS, false);
-                            mma_commit(&s_full[x]);
-                        }
+                        mma_kk<D / 16>(leader, tmem + kTmS + 128 * x, bq + x * C::TILE, bk + (nx % C::ST) * C::TILE, kS);
+                        commit(leader, &s_full[x]);
                     }
                 }
-                if (ok && lane == 0) {
-                    if (have_v) mma_commit(&v_empty[it % C::ST]);
-                    if (have_k) mma_commit(&k_empty[nx % C::ST]);
+                if (ok) {
+                    if (have_v) commit(leader, &v_empty[it % C::ST]);
+                    if (have_k) commit(leader, &k_empty[nx % C::ST]);
                 }
-                __syncwarp();
             }
-            if (s_abort) {  // products in flight end before the block frees its memory
-                if (lane == 0) {
-                    mma_commit(&bar_drain);
-                    mbar_wait(&bar_drain, 0, 1000000000ull);
-                }
-                __syncwarp();
-            }
+            if (s_abort) drain(leader, &bar_drain);
         } else if (warp == 9 && lane == 0 && g.je > g.jb) {  // ---- TMA loads
             prefetch_tmap(&maps.q);
             uint32_t bytes = 0;

@@ -50,24 +50,78 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// D (128 x N, fp32, TMEM) (+)= A (128 x 16 ks) B^T: both operands K-major SW128 tiles of `rows`
-// rows in column blocks of 64, A in shared memory.
-template <int kSteps, int kRowsA, int kRowsB>
-__device__ __forceinline__ void mma_kk(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc)
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect()
 {
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks)
-        tc::mma_ss(d, tc::sdesc_sw128(a + (ks >> 2) * (kRowsA * 128) + (ks & 3) * 32, 16, 1024),
-                   tc::sdesc_sw128(b + (ks >> 2) * (kRowsB * 128) + (ks & 3) * 32, 16, 1024), idesc, acc || ks > 0);
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
 }
-// D (128 x N) (+)= A B with A (128 x 16 ks, bf16) in TMEM and B a tile [16 ks rows][N channels] in
-// shared memory, N-major: column blocks of 64 channels kRows * 128 bytes apart.
-template <int kSteps, int kRows>
-__device__ __forceinline__ void mma_tn(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc)
+// Warp-uniform copies: the tensor core's instructions take their operands from uniform registers, and the
+// compiler keeps them there only where it can see that control flow and values are uniform.  A product
+// issued under `lane == 0` instead took 75 cycles, more than it runs.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// tcgen05.mma and commit by the lane that `leader` marks, in code that the whole warp runs
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
 {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], %2, %3, %4, p;\n\t}"
+        ::"r"(leader), "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%1], [%2], %3, %4, p;\n\t}"
+        ::"r"(leader), "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %0, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}"
+        ::"r"(leader), "r"(tc::smem_u32(bar))
+        : "memory");
+}
+
+// After a wait that gave up: products in flight end before the block frees its memory.
+__device__ __forceinline__ void drain(uint32_t leader, uint64_t *bar)
+{
+    commit(leader, bar);
+    tc::mbar_wait(bar, 0, 1000000000ull);
+    __syncwarp();
+}
+
+// D (128 x N, fp32, TMEM) (+)= A (128 x 16 ks) B^T: both operands K-major SW128 tiles in column blocks of
+// 64 channels, kBoxBytes apart.
+template <int kSteps>
+__device__ __forceinline__ void mma_kk(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc)
+{
+    const uint64_t da = tc::sdesc_sw128(a, 16, 1024), db = tc::sdesc_sw128(b, 16, 1024);
 #pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks)
-        tc::mma_ts(d, a + 8 * ks, tc::sdesc_sw128(b + ks * 2048, kRows * 128, 1024), idesc, acc || ks > 0);
+    for (int ks = 0; ks < kSteps; ++ks) {
+        const uint64_t off = (ks >> 2) * (kBoxBytes >> 4) + (ks & 3) * 2;  // in the descriptors' units of 16 bytes
+        mma_ss(leader, d, da + off, db + off, idesc, ks > 0);
+    }
+}
+// D (128 x N) (+)= A B with A (128 x 128, bf16) in TMEM, columns 64 .. of it kGap columns after the first 64's
+// 32, and B a tile [128 rows][N channels] in shared memory, N-major.
+template <int kGap>
+__device__ __forceinline__ void mma_tn(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
+{
+    const uint64_t db = tc::sdesc_sw128(b, kBoxBytes, 1024);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+        mma_ts(leader, d, a + (ks >> 2) * kGap + 8 * (ks & 3), db + ks * 128, idesc, ks > 0 ? 1u : acc);
 }
 
 // Zeros in rows [from, 128) of an SW128 tile of kBlocks column blocks, by one warp, visible to the
