@@ -3,6 +3,8 @@
 // (kv_cache.cu) and attention over it (attn_cached.cu).
 #pragma once
 
+#include <limits.h>
+
 #include "gdn2_internal.cuh"
 
 namespace gdn2 {
@@ -63,6 +65,61 @@ __device__ __forceinline__ bool find_tile(const SeqBatch &b, int tile, int per, 
         tile -= __shfl_sync(0xffffffffu, sum, 31);
     }
     return false;
+}
+// The rank'th tile in order of falling cost, so that the last blocks to run are the short ones.  A
+// tile costs the more the further it lies from its sequence's start (causal queries: the keys before
+// it) or, with from_end, from its end (keys: the queries after it): all sequences' tiles at the
+// greatest distance come first, then the next ones.  More than 32 packed sequences: in the batch's
+// order, their tiles are many and alike.  By a whole warp.
+__device__ __forceinline__ bool find_heavy_tile(const SeqBatch &b, int rank, int per, bool from_end, TileRef &r)
+{
+    if (!b.cu) {
+        const int nt = (b.T + per - 1) / per, d = nt - 1 - rank / b.n;
+        r.seq = rank % b.n;
+        r.tile = from_end ? nt - 1 - d : d;
+        r.sp = {r.seq * b.T, b.T};
+        return d >= 0;
+    }
+    if (b.n > 32) return find_tile(b, rank, per, r);
+    const int lane = threadIdx.x & 31;
+    SeqSpan sp = {0, -1};
+    if (lane < b.n) sp = batch_span(b, lane);
+    const int nt = sp.len > 0 ? (sp.len + per - 1) / per : 0;
+    auto beyond = [&](int d) { return __reduce_add_sync(0xffffffffu, max(nt - d, 0)); };  // tiles at distance >= d
+    int lo = 0, hi = __reduce_max_sync(0xffffffffu, nt);
+    if (beyond(0) <= rank) return false;
+    while (hi - lo > 1) {  // beyond(lo) > rank >= beyond(hi)
+        const int mid = (lo + hi) >> 1;
+        if (beyond(mid) > rank) lo = mid;
+        else hi = mid;
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, nt > lo);
+    r.seq = __fns(who, 0, rank - beyond(lo + 1) + 1);
+    r.sp.bos = __shfl_sync(0xffffffffu, sp.bos, r.seq);
+    r.sp.len = __shfl_sync(0xffffffffu, sp.len, r.seq);
+    r.tile = from_end ? __shfl_sync(0xffffffffu, nt, r.seq) - 1 - lo : lo;
+    return true;
+}
+// The same where a tile's cost is its sequence's `len` of keys: the longest sequences' tiles first.
+__device__ __forceinline__ bool find_long_tile(const SeqBatch &b, const int *lens, int rank, int per, TileRef &r)
+{
+    if (b.n > 32) return find_tile(b, rank, per, r);
+    const int lane = threadIdx.x & 31;
+    SeqSpan sp = {0, -1};
+    if (lane < b.n) sp = batch_span(b, lane);
+    const int nt = sp.len > 0 ? (sp.len + per - 1) / per : 0, len = nt ? lens[lane] : INT_MIN;
+    int before = 0;  // tiles of longer sequences
+    for (int i = 0; i < b.n; ++i) {
+        const int l = __shfl_sync(0xffffffffu, len, i), n = __shfl_sync(0xffffffffu, nt, i);
+        if (l > len || (l == len && i < lane)) before += n;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, rank >= before && rank < before + nt);
+    if (!hit) return false;
+    r.seq = __ffs(hit) - 1;
+    r.tile = rank - __shfl_sync(0xffffffffu, before, r.seq);
+    r.sp.bos = __shfl_sync(0xffffffffu, sp.bos, r.seq);
+    r.sp.len = __shfl_sync(0xffffffffu, sp.len, r.seq);
+    return true;
 }
 // upper bound of the number of tiles over all sequences
 inline long long tile_bound(const SeqBatch &b, int per)

@@ -14,6 +14,8 @@
 // Roles, 384 threads: warps 0-3 and 4-7 form p and ds of the tile's left and right 64 columns (a thread to
 // a row), warp 8 issues the products, warp 9 the TMA loads, warp 10 (keys' kernel) brings the rows'
 // lse and delta.  bf16 p and ds overwrite the columns of the scores that their own warps have read.
+#include <limits.h>
+
 #include "attn_tc.cuh"
 
 namespace gdn2 {
@@ -59,6 +61,12 @@ __device__ __forceinline__ void st64(uint32_t t, const float (&s)[64])
     for (int i = 0; i < 32; ++i) w[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
     tmem_st32(t, w);
     tmem_wait_st();
+}
+// D (+)= A B, A = 128 x 128 bf16 left by st64 of both column halves (64 columns apart)
+__device__ __forceinline__ void mma_grad(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
+{
+    mma_tn<4>(leader, d, a, b, 0, idesc, acc);
+    mma_tn<4>(leader, d, a + 64, b, 64, idesc, 1);
 }
 // f * (this thread's row of TMEM columns [0, n)) as bf16 at dst
 template <int n> __device__ __forceinline__ void store_row(uint32_t t, float f, __nv_bfloat16 *dst, bool live)
@@ -108,12 +116,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) report_bad_seqlens(p.b, p.status);
+    if (blockIdx.x == 0 && warp == 0) report_bad_seqlens(p.b, p.status);
     TileRef r;
-    if (!find_tile(p.b, gridDim.x - 1 - blockIdx.x, p.TQ, r)) return;
-    r.tile = uniform(r.tile);
-    r.sp.len = uniform(r.sp.len);
-    const int hk = blockIdx.y, len = r.sp.len, t0 = r.tile * p.TQ, nt = min(p.TQ, len - t0);
+    int hk;
+    if (!block_tile(p.b, blockIdx.x, gridDim.x / p.Hkv, p.Hkv, p.window, p.TQ, false, r, hk)) return;
+    const int len = r.sp.len, t0 = r.tile * p.TQ, nt = min(p.TQ, len - t0);
     const int jb = p.window == 0 || t0 < p.window ? 0 : (t0 - p.window + 1) / kBN, n = (t0 + nt - 1) / kBN + 1 - jb;
 
     if (tid == 0) {
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
             for (int it = 0; ok && it < n; ++it) {
                 if (!(ok = wait_warp(&ds_ready, it & 1, &s_abort, p.status))) break;
                 tc_fence_after();
-                mma_tn<64>(leader, tmem + kTmQ, tmem + 128 * (it & 1), bk + (it % C::KS) * C::TILE, kG, it > 0);
+                mma_grad(leader, tmem + kTmQ, tmem + 128 * (it & 1), bk + (it % C::KS) * C::TILE, kG, it > 0);
                 commit(leader, &k_empty[it % C::KS]);
                 if (it + 1 == n) commit(leader, &done);
                 if (it + 1 < n) ok = products(it + 1);
@@ -282,10 +289,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     TileRef r;
-    if (!find_tile(p.b, blockIdx.x, kBN, r)) return;
-    r.tile = uniform(r.tile);
-    r.sp.len = uniform(r.sp.len);
-    const int hk = blockIdx.y, len = r.sp.len, k0 = r.tile * kBN;
+    int hk;
+    if (!block_tile(p.b, blockIdx.x, gridDim.x / p.Hkv, p.Hkv, p.window, kBN, true, r, hk)) return;
+    const int len = r.sp.len, k0 = r.tile * kBN;
     // query tokens that see a key of this tile: k0 .. end - 1, in tiles of TQ from the sequence's start
     const int end = p.window == 0 || p.window > len ? len : min(len, k0 + kBN - 1 + p.window);
     const int ib = k0 / p.TQ, n = (end + p.TQ - 1) / p.TQ - ib;
@@ -394,12 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
                 const int st = it % C::ST;
                 if (!(ok = wait_warp(&p_ready, it & 1, &s_abort, p.status))) break;
                 tc_fence_after();
-                mma_tn<64>(leader, tmem + kTmV, tmem, bo + st * C::TILE, kG, it > 0);
+                mma_grad(leader, tmem + kTmV, tmem, bo + st * C::TILE, kG, it > 0);
                 commit(leader, &o_empty[st]);
                 if (it + 1 < n && !(ok = scores(it + 1))) break;
                 if (!(ok = wait_warp(&ds_ready, it & 1, &s_abort, p.status))) break;
                 tc_fence_after();
-                mma_tn<64>(leader, tmem + kTmK, tmem + kTmP, bq + st * C::TILE, kG, it > 0);
+                mma_grad(leader, tmem + kTmK, tmem + kTmP, bq + st * C::TILE, kG, it > 0);
                 commit(leader, &q_empty[st]);
                 if (it + 1 == n) commit(leader, &done);
                 if (it + 1 < n) ok = products(it + 1);
@@ -488,7 +494,9 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs &a, cudaStream_t s)
         return cudaErrorInvalidValue;
     cudaError_t e = launch_attn_delta(false, a, s);
     if (e != cudaSuccess) return e;
-    const dim3 gq((unsigned)tile_bound(a.b, p.TQ), (unsigned)a.Hkv), gk((unsigned)tile_bound(a.b, kBN), (unsigned)a.Hkv);
+    const long long nq = tile_bound(a.b, p.TQ) * a.Hkv, nk = tile_bound(a.b, kBN) * a.Hkv;
+    if (nq > INT_MAX || nk > INT_MAX) return cudaErrorInvalidValue;
+    const dim3 gq((unsigned)nq), gk((unsigned)nk);
     if (a.D == 128) {
         e = run(attn_dkv_tc_kernel<128>, DkvCfg<128>::SMEM, gk, maps, p, s);
         return e != cudaSuccess ? e : run(attn_dq_tc_kernel<128>, DqCfg<128>::SMEM, gq, maps, p, s);

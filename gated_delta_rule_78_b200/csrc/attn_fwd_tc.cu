@@ -10,10 +10,11 @@
 // ones); that costs 2^-9 of each weight, no more than the rounding of o.
 //
 // A block owns two tiles A and B of 128 packed query rows.  Roles: warps 0-3 and 4-7 the softmax of
-// A and of B (a thread to a row), warp 8 the products, warp 9 the TMA loads, warps 12-15 (paged
-// only) the gather of pages.  The tensor core works on one tile's S = Q K^T and O += P V while the
-// other tile's warps form its weights; P overwrites its own S in TMEM.  TMEM: S_A, S_B (128 columns
-// each), O_A, O_B (D columns each).
+// A and of B (a thread to a row), warp 8 the products, warp 9 the TMA loads, warps 9-11 (paged)
+// the gather of pages.  The tensor core works on one tile's S = Q K^T and O += P V while the other
+// tile's warps form its weights.  TMEM: S_A, S_B (128 columns each), O_A, O_B (D columns each).
+// With D = 128 that is all of it: P overwrites its own S, and the next S waits for P V.  With D = 64 P
+// has 64 columns of its own, and the next S is formed as soon as the warps hold this one in registers.
 #include <limits.h>
 
 #include "attn_tc.cuh"
@@ -57,9 +58,11 @@ template <int D> struct Cfg {
     static constexpr int NB = D / 64;                      // column blocks of a tile
     static constexpr int TILE = NB * kBoxBytes;            // bytes of a 128-row tile
     static constexpr int ST = D == 128 ? 2 : 4;            // stages of K and of V
-    static constexpr int SMEM = 2 * TILE + 2 * ST * TILE + 1024;
+    static constexpr int SMEM = 2 * TILE + 2 * ST * TILE + 1024;  // kPagedE4m3: and the raw rows
 };
-constexpr int kTmS = 0, kTmO = 256;  // TMEM columns: S_A, S_B; O_A, O_B
+template <int D> constexpr int kRawBytes = 64 * D;  // e4m3 rows of a step of the gather, three steps of them
+constexpr int kTmS = 0, kTmO = 256, kTmP = 384;  // TMEM columns: S_A, S_B; O_A, O_B; P_A, P_B (D = 64)
+constexpr int kThreads = 384, kGather = 3;  // threads; warps that gather pages
 constexpr float kGrow = 8.f;         // growth of the maximum (log2) that moves the reference
 
 struct FwdMaps {
@@ -72,7 +75,8 @@ struct FwdParams {
     __nv_bfloat16 *o;
     float *lse;
     int *status;
-    PagedCache c;       // paged only
+    PagedCache c;       // paged only, as is the rest
+    int box;            // rows of a box of a page
     float *part_o, *part_l;
 };
 
@@ -123,29 +127,41 @@ __device__ __forceinline__ Ranges make_ranges(const FwdParams &p, const TileRef 
     return g;
 }
 
-// Where the keys come from: whole sequences by TMA, or a paged cache's bf16 or e4m3 rows
-enum { kWhole, kPaged, kPagedE4m3 };
+// Where the keys come from: whole sequences by TMA; a paged cache's bf16 rows by TMA, in boxes of as
+// many rows as divide both a page and a tile (8 at least: a swizzle atom); pages of other sizes, and
+// e4m3 rows, by ordinary asynchronous copies.
+enum { kWhole, kPaged, kPagedAny, kPagedE4m3 };
 
 template <int D, int kind>
-__global__ void __launch_bounds__(kind != kWhole ? 512 : 384, 1) attn_fwd_tc_kernel(const __grid_constant__ FwdMaps maps,
+__global__ void __launch_bounds__(kThreads, 1) attn_fwd_tc_kernel(const __grid_constant__ FwdMaps maps,
                                                                           const __grid_constant__ FwdParams p)
 {
     using C = Cfg<D>;
-    constexpr bool paged = kind != kWhole, e4m3 = kind == kPagedE4m3;
-    constexpr int SS = C::ST + 1;  // stages of the scales: see the gather
+    constexpr bool kSep = D == 64;  // P beside S
+    constexpr bool paged = kind != kWhole, e4m3 = kind == kPagedE4m3, gather = kind >= kPagedAny;
+    constexpr int SS = C::ST + 2;  // stages of the scales: see the gather
     extern __shared__ char raw[];
     char *sm = reinterpret_cast<char *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     char *sq = sm, *sk = sm + 2 * C::TILE, *sv = sk + C::ST * C::TILE;
     __shared__ __align__(8) uint64_t bar_q, k_full[C::ST], k_empty[C::ST], v_full[C::ST], v_empty[C::ST], s_full[2],
-        p_ready[2], o_done[2], bar_drain;
+        s_free[2], p_ready[2][2], o_done[2], bar_drain;
     __shared__ uint32_t s_tmem;
     __shared__ float s_ks[e4m3 ? SS : 1][kBN], s_vs[e4m3 ? SS : 1][kBN];
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
-    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 0) report_bad_seqlens(p.b, p.status);
+    if (blockIdx.x == 0 && warp == 0) report_bad_seqlens(p.b, p.status);
     TileRef r;
-    if (!find_tile(p.b, gridDim.x - 1 - blockIdx.x, 2 * p.TQ, r)) return;
+    int hk, split = 0;
+    if constexpr (paged) {
+        hk = blockIdx.x % p.Hkv;
+        split = blockIdx.x / p.Hkv;
+        const int rank = split / p.splits;
+        split -= rank * p.splits;
+        if (!find_long_tile(p.b, p.c.kv_lens, rank, 2 * p.TQ, r)) return;
+    } else {
+        if (!block_tile(p.b, blockIdx.x, gridDim.x / p.Hkv, p.Hkv, p.window, 2 * p.TQ, false, r, hk)) return;
+    }
     int kvlen = r.sp.len;
     if (paged) {
         kvlen = p.c.kv_lens[r.seq];
@@ -154,22 +170,23 @@ __global__ void __launch_bounds__(kind != kWhole ? 512 : 384, 1) attn_fwd_tc_ker
             return;
         }
     }
-    const Ranges g = make_ranges(p, r, kvlen, blockIdx.z);
-    const int hk = blockIdx.y;
+    const Ranges g = make_ranges(p, r, kvlen, split);
 
     if (tid == 0) {
         s_abort = 0;
         mbar_init(&bar_q, 1);
         mbar_init(&bar_drain, 1);
         for (int i = 0; i < C::ST; ++i) {
-            mbar_init(&k_full[i], paged ? 128 : 1);
-            mbar_init(&v_full[i], paged ? 128 : 1);
+            mbar_init(&k_full[i], gather ? kGather * 32 : 1);
+            mbar_init(&v_full[i], gather ? kGather * 32 : 1);
             mbar_init(&k_empty[i], 1);
             mbar_init(&v_empty[i], 1);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s_full[x], 1);
-            mbar_init(&p_ready[x], 4);
+            mbar_init(&s_free[x], 4);
+            mbar_init(&p_ready[x][0], 4);
+            mbar_init(&p_ready[x][1], 4);
             mbar_init(&o_done[x], 1);
         }
         fence_mbar_init();
@@ -184,53 +201,62 @@ __global__ void __launch_bounds__(kind != kWhole ? 512 : 384, 1) attn_fwd_tc_ker
     const uint32_t tmem = uniform(s_tmem);
 
     if (warp < 8) {  // ---- softmax of tile A (warps 0-3) or B (4-7): thread = row
-        if constexpr (paged) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int x = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // TMEM lane 32 * (warp % 4)
         const uint32_t ts = tmem + kTmS + 128 * x + lanes, to = tmem + kTmO + D * x + lanes;
-        const int tok = row / p.G, gq = row - tok * p.G;
-        const int pos = g.first + g.t0[x] + tok;
-        const int low = g.first + g.t0[x], high = low + g.n[x] - 1;
+        const uint32_t tp = kSep ? tmem + kTmP + 64 * x + lanes : ts;
+        const int beg = x ? g.beg[1] : g.beg[0], end = x ? g.end[1] : g.end[0], nt = x ? g.n[1] : g.n[0];
+        const int tok0 = x ? g.t0[1] : g.t0[0], tok = row / p.G, gq = row - tok * p.G;
+        const int low = g.first + tok0, high = low + nt - 1, pos = low + tok;
         const float c = p.scale * kLog2e;
         float m = -INFINITY, l = 0.f;  // reference in units of s, sum of the weights relative to it
         bool ok = true;
         uint32_t ph = 0;
-        for (int j = g.beg[x]; j < g.end[x]; ++j, ph ^= 1) {
+        for (int j = beg; j < end; ++j, ph ^= 1) {
             if (!(ok = wait_warp(&s_full[x], ph, &s_abort, p.status))) break;
             tc_fence_after();
             float s[128];
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, reinterpret_cast<uint32_t(&)[32]>(s[32 * q]));
             tmem_wait_ld();
+            if constexpr (kSep) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_free[x]);
+            }
             const int k0 = j * kBN;
-            const float *vs = s_vs[0];
             if constexpr (e4m3) {
                 const float *ks = s_ks[(j - g.jb) % SS];
-                vs = s_vs[(j - g.jb) % SS];
 #pragma unroll
                 for (int i = 0; i < 128; ++i) s[i] *= ks[i];
             }
-            if (k0 + kBN - 1 > low || (p.window && k0 <= high - p.window)) {
+            const bool edge = k0 + kBN - 1 > low || (p.window && k0 <= high - p.window);
+            if (edge) {
                 const int most = pos - k0, least = p.window ? most - p.window + 1 : 0;
 #pragma unroll
                 for (int i = 0; i < 128; ++i) s[i] = i <= most && i >= least ? s[i] : -INFINITY;
             }
-            float t0 = s[0], t1 = s[1], t2 = s[2], t3 = s[3];
+            float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]), t2 = fmaxf(s[4], s[5]), t3 = fmaxf(s[6], s[7]);
 #pragma unroll
-            for (int i = 4; i < 128; i += 4) {
-                t0 = fmaxf(t0, s[i]);
-                t1 = fmaxf(t1, s[i + 1]);
-                t2 = fmaxf(t2, s[i + 2]);
-                t3 = fmaxf(t3, s[i + 3]);
+            for (int i = 8; i < 128; i += 8) {
+                t0 = max3(t0, s[i], s[i + 1]);
+                t1 = max3(t1, s[i + 2], s[i + 3]);
+                t2 = max3(t2, s[i + 4], s[i + 5]);
+                t3 = max3(t3, s[i + 6], s[i + 7]);
             }
-            const float top = fmaxf(fmaxf(t0, t1), fmaxf(t2, t3));
+            const float top = fmaxf(max3(t0, t1, t2), t3);
             const bool grow = (top - m) * c > kGrow;  // true for the row's first visible key (m = -inf)
-            if (__any_sync(0xffffffffu, grow)) {
+            const bool move = __any_sync(0xffffffffu, grow);
+            // P beside S: the former product has to be done with P and O (otherwise its commit came before
+            // this S)
+            if (kSep && j > beg && !(ok = wait_warp(&o_done[x], ph ^ 1, &s_abort, p.status))) break;
+            if (move) {
                 const float f = grow ? ex2((m - top) * c) : 1.f;
                 if (grow) m = top;
                 l *= f;
-                if (j > g.beg[x]) {  // the previous product is done: its commit came before this S
+                if (j > beg) {
+                    tc_fence_after();
 #pragma unroll
                     for (int q = 0; q < D / 32; ++q) {
                         uint32_t w[32];
@@ -243,35 +269,55 @@ __global__ void __launch_bounds__(kind != kWhole ? 512 : 384, 1) attn_fwd_tc_ker
                 }
             }
             const float off = m == -INFINITY ? 0.f : -m * c;  // no key visible yet: all weights 0
-            float sum0 = 0.f, sum1 = 0.f;
+            const uint64_t c2 = pair(c, c), off2 = pair(off, off);
+            uint64_t sum0 = 0, sum1 = 0;
+            // weights of a quarter of the keys, handed over as they are formed: the product starts on the
+            // first while the next are formed
+            auto weights = [&](int h) {
+                uint32_t w[16];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t w[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float a = ex2(fmaf(s[64 * q + 2 * i], c, off)), b = ex2(fmaf(s[64 * q + 2 * i + 1], c, off));
-                    sum0 += a;
-                    sum1 += b;
-                    if constexpr (e4m3) w[i] = pack_bf16x2(a * vs[64 * q + 2 * i], b * vs[64 * q + 2 * i + 1]);
-                    else w[i] = pack_bf16x2(a, b);
+                for (int i = 0; i < 16; ++i) {
+                    float a, b;
+                    unpair(fma2(pair(s[32 * h + 2 * i], s[32 * h + 2 * i + 1]), c2, off2), a, b);
+                    a = ex2(a);
+                    b = ex2(b);
+                    if (i & 1) sum1 = add2(sum1, pair(a, b));
+                    else sum0 = add2(sum0, pair(a, b));
+                    if constexpr (e4m3) {
+                        const float *vs = s_vs[(j - g.jb) % SS] + 32 * h;
+                        w[i] = pack_bf16x2(a * vs[2 * i], b * vs[2 * i + 1]);
+                    } else {
+                        w[i] = pack_bf16x2(a, b);
+                    }
                 }
-                tmem_st32(ts + 32 * q, w);
-            }
-            l += sum0 + sum1;
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready[x]);
+                tmem_st16(tp + 16 * h, w);
+            };
+            auto hand_over = [&](int h) {
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[x][h]);
+            };
+            weights(0);
+            weights(1);
+            hand_over(0);
+            weights(2);
+            weights(3);
+            hand_over(1);
+            float a, b, d, e;
+            unpair(sum0, a, b);
+            unpair(sum1, d, e);
+            l += (a + b) + (d + e);
         }
-        const bool any = g.beg[x] < g.end[x];
-        if (any && ok) ok = wait_warp(&o_done[x], 0, &s_abort, p.status);
-        if (ok && g.n[x] > 0) {  // (warp-uniform) o = O / l
+        const bool any = beg < end;
+        if (any && ok) ok = wait_warp(&o_done[x], kSep ? ph ^ 1 : 0, &s_abort, p.status);
+        if (ok && nt > 0) {  // (warp-uniform) o = O / l
             tc_fence_after();
-            const bool live = row < p.TQ * p.G && tok < g.n[x];
-            const size_t at = (size_t)(r.sp.bos + g.t0[x] + tok) * p.H + hk * p.G + gq;
+            const bool live = row < p.TQ * p.G && tok < nt;
+            const size_t at = (size_t)(r.sp.bos + tok0 + tok) * p.H + hk * p.G + gq;
             const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
             const float lse = l > 0.f || l != l ? (m * c + __log2f(l)) * kLn2 : -INFINITY;
-            const size_t base = p.splits > 1 ? ((size_t)blockIdx.z * p.b.rows * p.H + at) : at;
+            const size_t base = p.splits > 1 ? ((size_t)split * p.b.rows * p.H + at) : at;
 #pragma unroll
             for (int q = 0; q < D / 32; ++q) {
                 uint32_t w[32];
@@ -282,22 +328,21 @@ __global__ void __launch_bounds__(kind != kWhole ? 512 : 384, 1) attn_fwd_tc_ker
 #pragma unroll
                 for (int i = 0; i < 32; ++i) w[i] = any ? __float_as_uint(__uint_as_float(w[i]) * inv) : 0u;
                 if (!live) continue;
+                const size_t ch = base * D + 32 * q;
                 if (p.splits > 1) {
-                    float *dst = p.part_o + base * D + 32 * q;
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {
                         const uint32_t v[8] = {w[i], w[i + 1], w[i + 2], w[i + 3], w[i + 4], w[i + 5], w[i + 6], w[i + 7]};
-                        store32(dst + i, v);
+                        store32(p.part_o + ch + i, v);
                     }
                 } else {
-                    __nv_bfloat16 *dst = p.o + base * D + 32 * q;
 #pragma unroll
                     for (int i = 0; i < 32; i += 16) {
                         uint32_t v[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             v[e] = pack_bf16x2(__uint_as_float(w[i + 2 * e]), __uint_as_float(w[i + 2 * e + 1]));
-                        store32(dst + i, v);
+                        store32(p.o + ch + i, v);
                     }
                 }
             }
@@ -306,9 +351,8 @@ __global__ void __launch_bounds__(kind != kWhole ? 512 : 384, 1) attn_fwd_tc_ker
                 else if (p.lse) p.lse[base] = lse;
             }
         }
-    } else if (warp < 12) {
-        if constexpr (paged) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const uint32_t bq = smem_u32(sq), bk = smem_u32(sk), bv = smem_u32(sv);
         if (warp == 8) {  // ---- the products
             constexpr uint32_t kS = idesc_bf16(128, kBN, 0, 0), kO = idesc_bf16(128, D, 0, 1);
@@ -317,71 +361,133 @@ __global__ void __launch_bounds__(kind != kWhole ? 512 : 384, 1) attn_fwd_tc_ker
             uint32_t ph[2] = {0, 0};
             const int jb = uniform(g.jb), je = uniform(g.je), kvlen = uniform(g.kvlen);
             const int beg[2] = {uniform(g.beg[0]), uniform(g.beg[1])}, end[2] = {uniform(g.end[0]), uniform(g.end[1])};
+            // S of tile x for key tile `nx` in the ring
+            auto scores = [&](int x, int nx) {
+                tc_fence_after();
+                mma_kk<D / 16>(leader, tmem + kTmS + 128 * x, bq + x * C::TILE, bk + (nx % C::ST) * C::TILE, kS);
+                commit(leader, &s_full[x]);
+            };
+            // O += P V of tile x and key tile j = jb + it
+            auto output = [&](int x, int j, int it) {
+                const uint32_t tp = tmem + (kSep ? kTmP + 64 * x : kTmS + 128 * x);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!wait_warp(&p_ready[x][h], ph[x], &s_abort, p.status)) return false;
+                    tc_fence_after();
+                    mma_tn<4>(leader, tmem + kTmO + D * x, tp + 32 * h, bv + (it % C::ST) * C::TILE, 64 * h, kO, j > beg[x] || h);
+                }
+                ph[x] ^= 1;
+                if (kSep || j + 1 == end[x]) commit(leader, &o_done[x]);
+                return true;
+            };
+            auto have_v = [&](int it) {
+                if (!wait_warp(&v_full[it % C::ST], (it / C::ST) & 1, &s_abort, p.status)) return false;
+                if (kind == kPagedAny) fence_proxy_async_smem();  // the copies are ordinary writes to shared memory
+                // rows past the sequence hold other sequences' values: 0 * NaN is not 0
+                if (!gather && (jb + it + 1) * kBN > kvlen) zero_rows<C::NB>(sv + (it % C::ST) * C::TILE, kvlen - (jb + it) * kBN);
+                return true;
+            };
+            auto have_k = [&](int nx) {
+                if (!wait_warp(&k_full[nx % C::ST], (nx / C::ST) & 1, &s_abort, p.status)) return false;
+                if (kind == kPagedAny) fence_proxy_async_smem();
+                return true;
+            };
             for (int j = jb - 1; ok && j < je; ++j) {
                 const int it = j - jb, nx = it + 1;  // key tile j and the next one in the rings
-                bool have_v = false, have_k = false;
+                const bool now = j >= jb, next = j + 1 < je;
+                if constexpr (kSep) {
+                    if (next && !(ok = have_k(nx))) break;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (j >= beg[x] && j < end[x]) {
-                        if (!have_v) {
-                            if (!(ok = wait_warp(&v_full[it % C::ST], (it / C::ST) & 1, &s_abort, p.status))) break;
-                            // rows past the sequence hold other sequences' values: 0 * NaN is not 0
-                            if (!paged && (j + 1) * kBN > kvlen) zero_rows<C::NB>(sv + (it % C::ST) * C::TILE, kvlen - j * kBN);
-                            have_v = true;
-                        }
-                        if (!(ok = wait_warp(&p_ready[x], ph[x], &s_abort, p.status))) break;
-                        ph[x] ^= 1;
-                        tc_fence_after();
-                        mma_tn<32>(leader, tmem + kTmO + D * x, tmem + kTmS + 128 * x, bv + (it % C::ST) * C::TILE, kO, j > beg[x]);
-                        if (j + 1 == end[x]) commit(leader, &o_done[x]);
+                    for (int x = 0; x < 2; ++x) {
+                        if (!(j + 1 >= beg[x] && j + 1 < end[x])) continue;
+                        if (j >= beg[x] && !(ok = wait_warp(&s_free[x], ph[x], &s_abort, p.status))) break;
+                        scores(x, nx);
                     }
-                    if (j + 1 >= beg[x] && j + 1 < end[x]) {
-                        if (!have_k) {
-                            if (!(ok = wait_warp(&k_full[nx % C::ST], (nx / C::ST) & 1, &s_abort, p.status))) break;
-                            have_k = true;
-                        }
-                        tc_fence_after();
-                        mma_kk<D / 16>(leader, tmem + kTmS + 128 * x, bq + x * C::TILE, bk + (nx % C::ST) * C::TILE, kS);
-                        commit(leader, &s_full[x]);
+                    if (!ok) break;
+                    if (next) commit(leader, &k_empty[nx % C::ST]);
+                    if (now && !(ok = have_v(it))) break;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        if (j >= beg[x] && j < end[x] && !(ok = output(x, j, it))) break;
+                    if (!ok) break;
+                    if (now) commit(leader, &v_empty[it % C::ST]);
+                } else {
+                    if (now && !(ok = have_v(it))) break;
+                    if (next && !(ok = have_k(nx))) break;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (j >= beg[x] && j < end[x] && !(ok = output(x, j, it))) break;
+                        if (j + 1 >= beg[x] && j + 1 < end[x]) scores(x, nx);
                     }
-                }
-                if (ok) {
-                    if (have_v) commit(leader, &v_empty[it % C::ST]);
-                    if (have_k) commit(leader, &k_empty[nx % C::ST]);
+                    if (!ok) break;
+                    if (now) commit(leader, &v_empty[it % C::ST]);
+                    if (next) commit(leader, &k_empty[nx % C::ST]);
                 }
             }
             if (s_abort) drain(leader, &bar_drain);
-        } else if (warp == 9 && lane == 0 && g.je > g.jb) {  // ---- TMA loads
-            prefetch_tmap(&maps.q);
-            uint32_t bytes = 0;
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                if (g.n[x] > 0) bytes += C::NB * 128 * p.G * p.TQ;
-            mbar_expect_tx(&bar_q, bytes);
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                if (g.n[x] > 0)
-#pragma unroll
-                    for (int b = 0; b < C::NB; ++b)
-                        tma_load_3d(sq + x * C::TILE + b * kBoxBytes, &maps.q, 64 * b, hk * p.G, r.sp.bos + g.t0[x], &bar_q);
-            bool ok = true;
+        } else if (warp == 9 && g.je > g.jb) {  // ---- TMA loads
             int nk = 0, nv = 0;
-            if constexpr (!paged) {
-                for (int j = g.jb; ok && j < g.je; ++j) {
+            if (lane == 0) {
+                prefetch_tmap(&maps.q);
+                uint32_t bytes = 0;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (g.n[x] > 0) bytes += C::NB * 128 * p.G * p.TQ;
+                mbar_expect_tx(&bar_q, bytes);
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (g.n[x] > 0)
+#pragma unroll
+                        for (int b = 0; b < C::NB; ++b)
+                            tma_load_3d(sq + x * C::TILE + b * kBoxBytes, &maps.q, 64 * b, hk * p.G, r.sp.bos + g.t0[x], &bar_q);
+            }
+            if constexpr (kind == kWhole) {
+                for (int j = g.jb; lane == 0 && j < g.je; ++j) {
                     const int it = j - g.jb, s = it % C::ST;
                     const uint32_t par = ((it / C::ST) & 1) ^ 1;
-                    if (it >= C::ST && !(ok = wait(&k_empty[s], par, &s_abort, p.status))) break;
+                    if (it >= C::ST && !wait(&k_empty[s], par, &s_abort, p.status)) break;
                     mbar_expect_tx(&k_full[s], C::TILE);
 #pragma unroll
                     for (int b = 0; b < C::NB; ++b)
                         tma_load_3d(sk + s * C::TILE + b * kBoxBytes, &maps.k, 64 * b, hk, r.sp.bos + j * kBN, &k_full[s]);
                     ++nk;
-                    if (it >= C::ST && !(ok = wait(&v_empty[s], par, &s_abort, p.status))) break;
+                    if (it >= C::ST && !wait(&v_empty[s], par, &s_abort, p.status)) break;
                     mbar_expect_tx(&v_full[s], C::TILE);
 #pragma unroll
                     for (int b = 0; b < C::NB; ++b)
                         tma_load_3d(sv + s * C::TILE + b * kBoxBytes, &maps.v, 64 * b, hk, r.sp.bos + j * kBN, &v_full[s]);
                     ++nv;
+                }
+            }
+            if constexpr (kind == kPaged) {  // a box to a lane: column block `blk` of rows seg * box ..
+                __syncwarp();
+                const int seg = lane / C::NB, blk = lane % C::NB, off = blk * kBoxBytes + seg * p.box * 128;
+                const bool live = seg * p.box < kBN;
+                const int *table = p.c.table + (size_t)r.seq * p.c.width;
+                auto row_of = [&](int j) {  // its row in the cache, past the end (zeros) for what the sequence lacks
+                    const int at = j * kBN + seg * p.box, none = p.c.num_pages * p.c.page;
+                    if (!live || at >= g.kvlen) return none;
+                    const int pg = at / p.c.page, id = table[pg];
+                    if (id >= 0 && id < p.c.num_pages) return id * p.c.page + (at - pg * p.c.page);
+                    atomicExch(p.status, kStatusBadPages);
+                    return none;
+                };
+                int row = row_of(g.jb);
+                for (int j = g.jb; j < g.je; ++j) {
+                    const int it = j - g.jb, s = it % C::ST;
+                    const uint32_t par = ((it / C::ST) & 1) ^ 1;
+                    const int next = j + 1 < g.je ? row_of(j + 1) : 0;
+                    if (it >= C::ST && !wait_warp(&k_empty[s], par, &s_abort, p.status)) break;
+                    if (lane == 0) mbar_expect_tx(&k_full[s], C::TILE);
+                    __syncwarp();
+                    if (live) tma_load_3d(sk + s * C::TILE + off, &maps.k, 64 * blk, hk, row, &k_full[s]);
+                    ++nk;
+                    if (it >= C::ST && !wait_warp(&v_empty[s], par, &s_abort, p.status)) break;
+                    if (lane == 0) mbar_expect_tx(&v_full[s], C::TILE);
+                    __syncwarp();
+                    if (live) tma_load_3d(sv + s * C::TILE + off, &maps.v, 64 * blk, hk, row, &v_full[s]);
+                    ++nv;
+                    row = next;
                 }
             }
             // after a wait that gave up, loads in flight end before the block's memory is free
@@ -391,86 +497,114 @@ __global__ void __launch_bounds__(kind != kWhole ? 512 : 384, 1) attn_fwd_tc_ker
                 for (int i = max(0, nv - C::ST); i < nv; ++i) mbar_wait(&v_full[i % C::ST], (i / C::ST) & 1, 1000000000ull);
             }
         }
-    } else if constexpr (paged) {  // ---- the gather of cache rows, 32 rows of a tile to a warp
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        const int w4 = warp - 12;
-        const int *table = p.c.table + (size_t)r.seq * p.c.width;
-        // row w4 * 32 + lane of key tile j: its slot in the cache, -1 past the sequence
-        auto slot_of = [&](int j) {
-            const int at = j * kBN + w4 * 32 + lane;
-            if (at >= g.kvlen) return -1;
-            const int pg = at / p.c.page, id = table[pg];
-            if (id < 0 || id >= p.c.num_pages) {
-                atomicExch(p.status, kStatusBadPages);
-                return -1;
-            }
-            return id * p.c.page + (at - pg * p.c.page);
-        };
-        bool ok = true;
-        for (int j = g.jb; ok && j < g.je; ++j) {
-            const int it = j - g.jb, st = it % C::ST;
-            const uint32_t par = ((it / C::ST) & 1) ^ 1;
-            const int slot = slot_of(j);
-            if (it >= C::ST && !(ok = wait_warp(&k_empty[st], par, &s_abort, p.status))) break;
-            if constexpr (e4m3) {
-                // Stage it % SS of the scales is free: key stage `it` being empty, tile it - ST has been
-                // multiplied, for which the softmax of tile it - ST - 1 = it - SS was done.
-                s_ks[it % SS][w4 * 32 + lane] = slot >= 0 ? p.c.ks[(size_t)slot * p.Hkv + hk] : 0.f;
-                s_vs[it % SS][w4 * 32 + lane] = slot >= 0 ? p.c.vs[(size_t)slot * p.Hkv + hk] : 0.f;
-            }
-#pragma unroll 1
-            for (int isv = 0; isv < 2; ++isv) {
-                if (isv && it >= C::ST && !(ok = wait_warp(&v_empty[st], par, &s_abort, p.status))) break;
-                char *dst = (isv ? sv : sk) + st * C::TILE;
-                const char *src = static_cast<const char *>(isv ? p.c.v : p.c.k);
+        if constexpr (gather) {
+            if (warp >= 9) {  // ---- the gather of cache rows
+                __syncwarp();
+                const int w = warp - 9;
+                const int *table = p.c.table + (size_t)r.seq * p.c.width;
+                constexpr int CH = e4m3 ? D / 16 : D / 8, RP = 32 / CH;  // 16-byte chunks of a row, rows a pass
+                const int ch = lane % CH;
+                // rows lane + 32 i of a key tile: their slots in the cache, -1 past the sequence
+                auto find_slots = [&](int j, int (&slot)[4]) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = j * kBN + 32 * i + lane;
+                        slot[i] = -1;
+                        if (at >= g.kvlen) continue;
+                        const int pg = at / p.c.page, id = table[pg];
+                        if (id >= 0 && id < p.c.num_pages) slot[i] = id * p.c.page + (at - pg * p.c.page);
+                        else atomicExch(p.status, kStatusBadPages);
+                    }
+                };
+                // copies this warp's share of 64 rows, slots s0 and s1 of each lane; put(row) says where a chunk goes
+                auto copy = [&](int s0, int s1, const void *cache, auto put) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll 4
+                        for (int q = (w + i) % kGather; q < CH; q += kGather) {  // 32 rows are CH passes
+                            const int in = q * RP + lane / CH, s = __shfl_sync(0xffffffffu, i ? s1 : s0, in);
+                            const char *from = static_cast<const char *>(cache) + ((size_t)max(s, 0) * p.Hkv + hk) * (CH * 16) + ch * 16;
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(put(32 * i + in))), "l"(from),
+                                         "r"(s >= 0 ? 16 : 0)
+                                         : "memory");
+                        }
+                };
+                int slot[4];
+                bool ok = true;
                 if constexpr (!e4m3) {
-                    constexpr int CH = D / 8, RP = 32 / CH;  // 16-byte chunks of a row, rows a pass
-                    const int ch = lane % CH;
-#pragma unroll
-                    for (int i = 0; i < 32 / RP; ++i) {
-                        const int row = i * RP + lane / CH, s = __shfl_sync(0xffffffffu, slot, row);
-                        const char *from = src + (((size_t)max(s, 0) * p.Hkv + hk) * D + ch * 8) * 2;
-                        const uint32_t to = smem_u32(dst + (ch >> 3) * kBoxBytes) + sw128(w4 * 32 + row, (ch & 7) * 16);
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(s >= 0 ? 16 : 0)
-                                     : "memory");
+                    // straight into the tiles; a stage's barrier counts every thread's copies as they land
+                    for (int j = g.jb; ok && j < g.je; ++j) {
+                        const int it = j - g.jb, st = it % C::ST;
+                        const uint32_t par = ((it / C::ST) & 1) ^ 1;
+                        find_slots(j, slot);
+#pragma unroll 1
+                        for (int isv = 0; isv < 2; ++isv) {
+                            if (it >= C::ST && !(ok = wait_warp(isv ? &v_empty[st] : &k_empty[st], par, &s_abort, p.status))) break;
+                            char *dst = (isv ? sv : sk) + st * C::TILE + (ch >> 3) * kBoxBytes;
+                            const void *cache = isv ? p.c.v : p.c.k;
+                            copy(slot[0], slot[1], cache, [&](int row) { return dst + sw128(row, (ch & 7) * 16); });
+                            copy(slot[2], slot[3], cache, [&](int row) { return dst + sw128(64 + row, (ch & 7) * 16); });
+                            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                                             smem_u32(isv ? &v_full[st] : &k_full[st]))
+                                         : "memory");
+                        }
                     }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
-                    // the copies before these have landed: V of the tile before, or K of this one
-                    asm volatile("cp.async.wait_group 1;" ::: "memory");
-                    fence_proxy_async_smem();
-                    if (isv) mbar_arrive(&k_full[st]);
-                    else if (it > 0) mbar_arrive(&v_full[(it - 1) % C::ST]);
                 } else {
-                    constexpr int CH = D / 16, RP = 32 / CH;  // 16 channels of 8 bits a lane
-                    const int ch = lane % CH;
-                    uint4 x[32 / RP];
+                    // by way of raw rows in shared memory, 64 a step (K, K, V, V of a tile), two steps' copies in
+                    // flight while a third becomes bf16; a lane converts the chunks that it has copied
+                    char *raw8 = sv + C::ST * C::TILE;
+                    auto fetch = [&](int h) {
+                        if (h < 4 * (g.je - g.jb)) {
+                            if (!(h & 3)) find_slots(g.jb + h / 4, slot);
+                            char *dst = raw8 + h % 3 * kRawBytes<D> + ch * 16;
+                            copy(h & 1 ? slot[2] : slot[0], h & 1 ? slot[3] : slot[1], h & 2 ? p.c.v : p.c.k,
+                                 [&](int row) { return dst + row * D; });
+                        }
+                        asm volatile("cp.async.commit_group;" ::: "memory");
+                    };
+                    fetch(0);
+                    fetch(1);
+                    for (int h = 0; ok && h < 4 * (g.je - g.jb); ++h) {
+                        const int it = h / 4, isv = h & 2, st = it % C::ST;
+                        if (!(h & 1) && it >= C::ST &&
+                            !(ok = wait_warp(isv ? &v_empty[st] : &k_empty[st], ((it / C::ST) & 1) ^ 1, &s_abort, p.status)))
+                            break;
+                        if (!(h & 3)) {
+                            // Stage it % SS of the scales is free: with key stage `it` empty S of tile it - ST is
+                            // formed, before which the weights of tile it - ST - 2 = it - SS were handed over (with
+                            // P over S even those of the tile after).
 #pragma unroll
-                    for (int i = 0; i < 32 / RP; ++i) {
-                        const int s = __shfl_sync(0xffffffffu, slot, i * RP + lane / CH);
-                        x[i] = make_uint4(0, 0, 0, 0);
-                        if (s >= 0) x[i] = *reinterpret_cast<const uint4 *>(src + ((size_t)s * p.Hkv + hk) * D + ch * 16);
-                    }
+                            for (int i = 0; i < 4; ++i) {
+                                if (i % kGather != w) continue;
+                                const size_t from = (size_t)max(slot[i], 0) * p.Hkv + hk;
+                                s_ks[it % SS][32 * i + lane] = slot[i] >= 0 ? p.c.ks[from] : 0.f;
+                                s_vs[it % SS][32 * i + lane] = slot[i] >= 0 ? p.c.vs[from] : 0.f;
+                            }
+                        }
+                        fetch(h + 2);
+                        asm volatile("cp.async.wait_group 2;" ::: "memory");
+                        const char *src = raw8 + h % 3 * kRawBytes<D> + ch * 16;
+                        char *dst = (isv ? sv : sk) + st * C::TILE + (ch >> 2) * kBoxBytes;
 #pragma unroll
-                    for (int i = 0; i < 32 / RP; ++i) {
-                        const int row = w4 * 32 + i * RP + lane / CH;
-                        uint32_t y[8];
-                        e4m3x4_bf16(x[i].x, y[0], y[1]);
-                        e4m3x4_bf16(x[i].y, y[2], y[3]);
-                        e4m3x4_bf16(x[i].z, y[4], y[5]);
-                        e4m3x4_bf16(x[i].w, y[6], y[7]);
-                        char *to = dst + (ch >> 2) * kBoxBytes;
-                        *reinterpret_cast<uint4 *>(to + sw128(row, (ch & 3) * 32)) = make_uint4(y[0], y[1], y[2], y[3]);
-                        *reinterpret_cast<uint4 *>(to + sw128(row, (ch & 3) * 32 + 16)) = make_uint4(y[4], y[5], y[6], y[7]);
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll 2
+                            for (int q = (w + i) % kGather; q < CH; q += kGather) {
+                                const int in = 32 * i + q * RP + lane / CH, row = 64 * (h & 1) + in;
+                                const uint4 x = *reinterpret_cast<const uint4 *>(src + in * D);
+                                uint32_t z[8];
+                                e4m3x4_bf16(x.x, z[0], z[1]);
+                                e4m3x4_bf16(x.y, z[2], z[3]);
+                                e4m3x4_bf16(x.z, z[4], z[5]);
+                                e4m3x4_bf16(x.w, z[6], z[7]);
+                                *reinterpret_cast<uint4 *>(dst + sw128(row, (ch & 3) * 32)) = make_uint4(z[0], z[1], z[2], z[3]);
+                                *reinterpret_cast<uint4 *>(dst + sw128(row, (ch & 3) * 32 + 16)) = make_uint4(z[4], z[5], z[6], z[7]);
+                            }
+                        fence_proxy_async_smem();
+                        if (h & 1) mbar_arrive(isv ? &v_full[st] : &k_full[st]);
                     }
-                    fence_proxy_async_smem();
-                    mbar_arrive(isv ? &v_full[st] : &k_full[st]);
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
             }
-        }
-        if constexpr (!e4m3) {
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            fence_proxy_async_smem();
-            if (ok && g.je > g.jb) mbar_arrive(&v_full[(g.je - 1 - g.jb) % C::ST]);
         }
     }
     tc_fence_before();
@@ -484,9 +618,10 @@ __global__ void __launch_bounds__(kind != kWhole ? 512 : 384, 1) attn_fwd_tc_ker
 template <int D, int kind> cudaError_t run(const FwdMaps &maps, const FwdParams &p, dim3 grid, cudaStream_t s)
 {
     auto kernel = attn_fwd_tc_kernel<D, kind>;
-    cudaError_t e = set_smem_attr(reinterpret_cast<const void *>(kernel), Cfg<D>::SMEM);
+    constexpr int smem = Cfg<D>::SMEM + (kind == kPagedE4m3 ? 3 * kRawBytes<D> : 0);
+    cudaError_t e = set_smem_attr(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kind != kWhole ? 512 : 384, Cfg<D>::SMEM, s>>>(maps, p);
+    kernel<<<grid, kThreads, smem, s>>>(maps, p);
     return cudaGetLastError();
 }
 
@@ -511,7 +646,9 @@ cudaError_t launch_attn_fwd_tc(const AttnArgs &a, cudaStream_t s)
         !make_head_map(&maps.k, a.k, a.b.rows, a.Hkv, a.D, 1, kBN) ||
         !make_head_map(&maps.v, a.v, a.b.rows, a.Hkv, a.D, 1, kBN))
         return cudaErrorInvalidValue;
-    const dim3 grid((unsigned)tile_bound(a.b, 2 * p.TQ), (unsigned)a.Hkv);
+    const long long blocks = tile_bound(a.b, 2 * p.TQ) * a.Hkv;
+    if (blocks > INT_MAX) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)blocks);
     return a.D == 128 ? run<128, kWhole>(maps, p, grid, s) : run<64, kWhole>(maps, p, grid, s);
 }
 
@@ -534,10 +671,19 @@ cudaError_t launch_attn_cached_tc(const CachedArgs &a, cudaStream_t s)
     p.part_o = a.part_o;
     p.part_l = a.part_l;
     if (!make_head_map(&maps.q, a.q, a.b.rows, a.H, a.D, p.G, p.TQ)) return cudaErrorInvalidValue;
-    maps.k = maps.v = maps.q;  // not read
-    const dim3 grid((unsigned)tile_bound(a.b, 2 * p.TQ), (unsigned)a.Hkv, (unsigned)a.splits);
+    maps.k = maps.v = maps.q;  // not read, but by kPaged
+    p.box = kBN;
+    while (p.box > 1 && a.c.page % p.box) p.box >>= 1;
+    if (!a.c.e4m3 && p.box >= 8 &&
+        (!make_head_map(&maps.k, a.c.k, (long long)a.c.num_pages * a.c.page, a.Hkv, a.D, 1, p.box) ||
+         !make_head_map(&maps.v, a.c.v, (long long)a.c.num_pages * a.c.page, a.Hkv, a.D, 1, p.box)))
+        return cudaErrorInvalidValue;
+    const long long blocks = tile_bound(a.b, 2 * p.TQ) * a.Hkv * a.splits;
+    if (blocks > INT_MAX) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)blocks);
     if (a.c.e4m3) return a.D == 128 ? run<128, kPagedE4m3>(maps, p, grid, s) : run<64, kPagedE4m3>(maps, p, grid, s);
-    return a.D == 128 ? run<128, kPaged>(maps, p, grid, s) : run<64, kPaged>(maps, p, grid, s);
+    if (p.box >= 8) return a.D == 128 ? run<128, kPaged>(maps, p, grid, s) : run<64, kPaged>(maps, p, grid, s);
+    return a.D == 128 ? run<128, kPagedAny>(maps, p, grid, s) : run<64, kPagedAny>(maps, p, grid, s);
 }
 
 }  // namespace gdn2

@@ -113,15 +113,14 @@ __device__ __forceinline__ void mma_kk(uint32_t leader, uint32_t d, uint32_t a, 
         mma_ss(leader, d, da + off, db + off, idesc, ks > 0);
     }
 }
-// D (128 x N) (+)= A B with A (128 x 128, bf16) in TMEM, columns 64 .. of it kGap columns after the first 64's
-// 32, and B a tile [128 rows][N channels] in shared memory, N-major.
-template <int kGap>
-__device__ __forceinline__ void mma_tn(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
+// D (128 x N) (+)= A B with A (128 x 16 ks, bf16, 8 columns a step) in TMEM and B the same number of rows, from
+// `row` on, of a tile [128 rows][N channels] in shared memory, N-major.
+template <int kSteps>
+__device__ __forceinline__ void mma_tn(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, int row, uint32_t idesc, uint32_t acc)
 {
-    const uint64_t db = tc::sdesc_sw128(b, kBoxBytes, 1024);
+    const uint64_t db = tc::sdesc_sw128(b + row * 128, kBoxBytes, 1024);
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
-        mma_ts(leader, d, a + (ks >> 2) * kGap + 8 * (ks & 3), db + ks * 128, idesc, ks > 0 ? 1u : acc);
+    for (int ks = 0; ks < kSteps; ++ks) mma_ts(leader, d, a + 8 * ks, db + ks * 128, idesc, ks > 0 ? 1u : acc);
 }
 
 // Zeros in rows [from, 128) of an SW128 tile of kBlocks column blocks, by one warp, visible to the
@@ -136,6 +135,35 @@ template <int kBlocks> __device__ __forceinline__ void zero_rows(char *tile, int
     __syncwarp();
 }
 
+// Pairs of fp32 values: one instruction to two of them.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 // Four e4m3 values as two pairs of bf16 (exact: e4m3 -> f16 -> f32 -> bf16).
 __device__ __forceinline__ void e4m3x4_bf16(uint32_t x, uint32_t &lo, uint32_t &hi)
 {
@@ -147,6 +175,29 @@ __device__ __forceinline__ void e4m3x4_bf16(uint32_t x, uint32_t &lo, uint32_t &
     const float2 f1 = __half22float2(*reinterpret_cast<const __half2 *>(&h1));
     lo = tc::pack_bf16x2(f0.x, f0.y);
     hi = tc::pack_bf16x2(f1.x, f1.y);
+}
+
+// The tile and key head of block `block` of a grid of tiles * Hkv blocks.  Without a window tiles differ
+// in cost by their length: the heavy ones first, all heads' together.  With a window almost all cost
+// the same, and a head's neighbouring tiles, which share most of their keys, run together: K and V of
+// all heads at once do not stay in L2 (4 x 4096, 16 heads, window 2048: forward, dk/dv and dq take
+// 8 to 10% longer heavy-first; the other way round a causal dk/dv at d = 64 takes 40% longer).
+__device__ __forceinline__ bool block_tile(const SeqBatch &b, int block, int tiles, int Hkv, int window, int per, bool from_end,
+                                           TileRef &r, int &head)
+{
+    bool ok;
+    if (window) {
+        head = block / tiles;
+        const int i = block - head * tiles;
+        ok = find_tile(b, from_end ? i : tiles - 1 - i, per, r);
+    } else {
+        head = block % Hkv;
+        ok = find_heavy_tile(b, block / Hkv, per, from_end, r);
+    }
+    head = uniform(head);
+    r.tile = uniform(r.tile);
+    r.sp.len = uniform(r.sp.len);
+    return ok;
 }
 
 // TMA view of a bf16 [rows][heads][D] tensor: boxes of (64 channels, box_heads, box_rows).
