@@ -2,11 +2,15 @@
 // steps), and the joining of parts.
 //
 // A decode step reads every visible key and value once and computes 4 D flop a pair for the G query
-// heads of a key head: it is bound by memory.  A block takes 16 packed query rows (row r is token
-// r / G, head r % G) and one part of the key axis; its 4 warps take key steps of 16 in turn, each with
-// a ring of its own of cp.async stages, so that no warp waits for another until the end, where their
-// sums are joined in shared memory.  Products are m16n8k16 (16 rows are all there is: a 128-row tile
-// of the fifth-generation tensor core would be 7/8 empty and the time is the loads').
+// heads of a key head: it is bound by memory.  A block takes 8 packed query rows (row r is token r / G,
+// head r % G; 16 where sequences bring more than 8) and one part of the key axis; its 4 warps take key
+// steps in turn, each with a ring of its own of cp.async stages, so that no warp waits for another
+// until the end, where their sums are joined in shared memory.
+//
+// Products are m16n8k16 on transposed operands: S^T = K Q^T and O^T = V^T P^T, keys and channels in the
+// 16 rows and queries in the 8 columns.  The other way round a decode step's few queries leave three
+// quarters of the 16 rows empty, with twice the products, registers and exponentials.  (A 128-row tile of
+// the fifth-generation tensor core would be emptier still, and the time is the loads'.)
 //
 // e4m3 rows go to shared memory as they are and become f16 in registers, one conversion to two values
 // (by way of f32 to bf16 it would be four).  f16 holds every e4m3 value.  Its range asks for care on
@@ -28,18 +32,20 @@ using attn::kLog2e;
 using tc::pack_bf16x2;
 using tc::smem_u32;
 
-constexpr int kWarps = 4, kRows = 16, kStep = 16;  // warps, query rows, keys of a warp's step
+constexpr int kWarps = 4;
 constexpr float kGrow = 8.f;    // growth of the maximum (log2) that moves the reference
 constexpr float kWeight = 6.f;  // e4m3: log2 of the weight at the reference
 
-template <int D, bool e4m3> struct Cfg {
+template <int D, bool e4m3, int NQ> struct Cfg {
+    static constexpr int ROWS = 8 * NQ;                    // query rows
+    static constexpr int STEP = e4m3 ? 32 : 16;            // keys of a warp's step
     static constexpr int ROW = D * (e4m3 ? 1 : 2);         // bytes of a cache row
-    static constexpr int TILE = kStep * ROW;               // a warp's K (or V) stage
-    static constexpr int SCALES = e4m3 ? 2 * kStep * 4 : 0;
+    static constexpr int TILE = STEP * ROW;                // a warp's K (or V) stage
+    static constexpr int SCALES = e4m3 ? 2 * STEP * 4 : 0;
     static constexpr int STAGE = 2 * TILE + SCALES;
-    static constexpr int ST = e4m3 ? 4 : D == 128 ? 3 : 4;
+    static constexpr int ST = D == 128 ? (e4m3 ? 2 : 3) : (e4m3 ? 3 : 4);
     static constexpr int RING = kWarps * ST * STAGE;
-    static constexpr int MERGE = kWarps * kRows * (D + 4) * 4;  // the warps' outputs, over the rings
+    static constexpr int MERGE = kWarps * ROWS * (D + 4) * 4;  // the warps' outputs, over the rings
     static constexpr int SMEM = RING > MERGE ? RING : MERGE;
 };
 
@@ -86,6 +92,13 @@ __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr)
                  : "r"(addr)
                  : "memory");
 }
+// the transpose of an 8 x 8 matrix of 16-bit values, a row to four lanes
+__device__ __forceinline__ uint32_t transpose(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 __device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -102,8 +115,8 @@ template <int ROW> __device__ __forceinline__ uint32_t chunk(int r, int c)
 }
 
 // Block x < n is the first tile of sequence x; the others are the further tiles of sequences with
-// more than 16 rows, in order.  By a whole warp.
-__device__ __forceinline__ bool find_rows(const Params &p, int x, TileRef &r)
+// more than `rows` rows, in order.  By a whole warp.
+__device__ __forceinline__ bool find_rows(const Params &p, int x, int rows, TileRef &r)
 {
     if (x < p.b.n) {
         r.seq = x;
@@ -116,7 +129,7 @@ __device__ __forceinline__ bool find_rows(const Params &p, int x, TileRef &r)
     for (int base = 0; base < p.b.n; base += 32) {
         SeqSpan sp = {0, -1};
         if (base + lane < p.b.n) sp = batch_span(p.b, base + lane);
-        const int more = sp.len > 0 ? (int)(((long long)sp.len * p.G + kRows - 1) / kRows) - 1 : 0;
+        const int more = sp.len > 0 ? (int)(((long long)sp.len * p.G + rows - 1) / rows) - 1 : 0;
         int sum = more;
 #pragma unroll
         for (int m = 1; m < 32; m <<= 1) {
@@ -137,15 +150,16 @@ __device__ __forceinline__ bool find_rows(const Params &p, int x, TileRef &r)
     return false;
 }
 
-template <int D, bool e4m3>
+template <int D, bool e4m3, int NQ>
 __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_constant__ Params p)
 {
-    using C = Cfg<D, e4m3>;
+    using C = Cfg<D, e4m3, NQ>;
+    constexpr int kStep = C::STEP, KT = kStep / 16, kRows = C::ROWS;  // keys of a step, tiles of 16 of them, query rows
     extern __shared__ __align__(128) char sm[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 0) report_bad_seqlens(p.b, p.status);
     TileRef r;
-    if (!find_rows(p, blockIdx.x, r)) return;
+    if (!find_rows(p, blockIdx.x, kRows, r)) return;
     const int kvlen = p.c.kv_lens[r.seq], first = kvlen - r.sp.len;
     if (first < 0 || kvlen > (long long)p.c.width * p.c.page) {
         if (tid == 0) atomicExch(p.status, kStatusBadPages);
@@ -166,74 +180,52 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
         return;
     }
 
-    // Q fragments: rows g and g + 8.  e4m3 keys come four channels to a lane (see below), so there a
-    // lane's k indices 2t, 2t+1, 2t+8, 2t+9 stand for channels 4t .. 4t+3; a sum has no order.
-    uint32_t qf[D / 16][4];
-    float qscale[2] = {1.f, 1.f};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int row = g + 8 * i;
-        const __nv_bfloat16 *q = p.q + row_at(min(row, rows - 1)) * D;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                qf[k][i + 2 * e] = *reinterpret_cast<const uint32_t *>(q + 16 * k + (e4m3 ? 4 * t + 2 * e : 2 * t + 8 * e));
-        if constexpr (e4m3) {  // f16 of q 2^-x, x from the row's largest finite exponent
-            uint32_t top = 0;
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t w = qf[k][i + 2 * e], lo = (w >> 7) & 0xffu, hi = (w >> 23) & 0xffu;
-                    top = max(top, max(lo < 255u ? lo : 0u, hi < 255u ? hi : 0u));
-                }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int x = min(max((int)top - 127 - 13, -120), 120);
-            const float f = __uint_as_float((uint32_t)(127 - x) << 23);
-            qscale[i] = __uint_as_float((uint32_t)(127 + x) << 23);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t w = qf[k][i + 2 * e];
-                    qf[k][i + 2 * e] = pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
-                }
-        }
-    }
-    int pos[2];  // positions of this lane's two rows
-#pragma unroll
-    for (int i = 0; i < 2; ++i) pos[i] = g + 8 * i < rows ? first + (r0 + g + 8 * i) / p.G : -1;
-
     const int *table = p.c.table + (size_t)r.seq * p.c.width;
     char *ring = sm + warp * C::ST * C::STAGE;
     const int nsteps = (ke - kb + kStep - 1) / kStep, mine = nsteps > warp ? (nsteps - warp + kWarps - 1) / kWarps : 0;
-    // keys kb + 16 (warp + 4 i) .. of this warp's step i into its stage i % ST; rows past the part and
-    // rows of bad pages become zeros
+    // The keys of this warp's step i, from kb + kStep (warp + 4 i) on, go into its stage i % ST; rows past
+    // the part and rows of bad pages become zeros.  Lane l looks up row l % kStep: `pg` and `in` are its
+    // page and place for the next step to load, carried from step to step without a division, and `id` is
+    // that page's table entry, read a step ahead.
+    constexpr int CH = C::ROW / 16, RP = 32 / CH;
+    const int ch = lane % CH;
+    const char *kbase = (const char *)p.c.k + (size_t)hk * C::ROW + ch * 16, *vbase = (const char *)p.c.v + (size_t)hk * C::ROW + ch * 16;
+    const uint32_t rowbytes = (uint32_t)p.Hkv * C::ROW;
+    const uint32_t to0 = smem_u32(ring) + chunk<C::ROW>(lane / CH, ch);
+    int at = kb + kStep * warp + lane % kStep, pg = at / p.c.page, in = at - pg * p.c.page;
+    const int dpg = kStep * kWarps / p.c.page, din = kStep * kWarps - dpg * p.c.page;
+    int id = at < ke ? table[pg] : -1;
     auto load = [&](int i) {
         if (i < mine) {
-            const int at = kb + kStep * (warp + kWarps * i) + (lane & 15);
             int slot = -1;
             if (at < ke) {
-                const int pg = at / p.c.page, id = table[pg];
-                if (id >= 0 && id < p.c.num_pages) slot = id * p.c.page + (at - pg * p.c.page);
+                if (id >= 0 && id < p.c.num_pages) slot = id * p.c.page + in;
                 else atomicExch(p.status, kStatusBadPages);
             }
-            char *st = ring + (i % C::ST) * C::STAGE;
-            constexpr int CH = C::ROW / 16, RP = 32 / CH;
-            const int ch = lane % CH;
+            at += kStep * kWarps;
+            pg += dpg;
+            in += din;
+            if (in >= p.c.page) {
+                in -= p.c.page;
+                ++pg;
+            }
+            id = at < ke ? table[pg] : -1;
+            const uint32_t st = (uint32_t)(i % C::ST) * C::STAGE;
 #pragma unroll
             for (int x = 0; x < kStep / RP; ++x) {
-                const int row = x * RP + lane / CH, s = __shfl_sync(0xffffffffu, slot, row);
-                const size_t off = ((size_t)max(s, 0) * p.Hkv + hk) * C::ROW + ch * 16;
-                const uint32_t to = smem_u32(st) + chunk<C::ROW>(row, ch), n = s >= 0 ? 16 : 0;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"((const char *)p.c.k + off), "r"(n) : "memory");
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + C::TILE), "l"((const char *)p.c.v + off), "r"(n) : "memory");
+                const int s = __shfl_sync(0xffffffffu, slot, x * RP + lane / CH);
+                const size_t off = (size_t)(uint32_t)max(s, 0) * rowbytes;
+                // the chunk permutation repeats every 8 rows
+                const uint32_t to = RP % 8 == 0 ? to0 + st + x * RP * C::ROW : smem_u32(ring) + st + chunk<C::ROW>(x * RP + lane / CH, ch);
+                const uint32_t n = s >= 0 ? 16 : 0;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(kbase + off), "r"(n) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + C::TILE), "l"(vbase + off), "r"(n) : "memory");
             }
-            if constexpr (e4m3) {  // lanes 0-15 the keys' scales, 16-31 the values'
-                const float *sc = (lane < 16 ? p.c.ks : p.c.vs) + (size_t)max(slot, 0) * p.Hkv + hk;
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(st + 2 * C::TILE) + 4 * lane), "l"(sc), "r"(slot >= 0 ? 4 : 0) : "memory");
+            if constexpr (e4m3) {
+                const size_t off = (size_t)max(slot, 0) * p.Hkv + hk;
+                const uint32_t to = smem_u32(ring) + st + 2 * C::TILE + 4 * lane, n = slot >= 0 ? 4 : 0;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(p.c.ks + off), "r"(n) : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 4 * kStep), "l"(p.c.vs + off), "r"(n) : "memory");
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -241,164 +233,246 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < C::ST - 1; ++i) load(i);
 
-    // m: reference of the sums l, wm: of the outputs o (the same without a scale of values); log2
-    float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, wm[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // Q fragments: column g of each tile of 8 queries.  e4m3 keys come four channels to a lane (see below),
+    // so there a lane's k indices 2t, 2t+1, 2t+8, 2t+9 stand for channels 4t .. 4t+3; a sum has no order.
+    uint32_t qf[D / 16][NQ][2];
+    float cq[NQ][2];  // scale log2 e (and a row's power of two) of columns 2t, 2t + 1
+    int pos[NQ][2];   // their positions
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
+    for (int n = 0; n < NQ; ++n) {
+        const __nv_bfloat16 *q = p.q + row_at(min(g + 8 * n, rows - 1)) * D;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-    const float c = p.scale * kLog2e;
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                qf[k][n][e] = *reinterpret_cast<const uint32_t *>(q + 16 * k + (e4m3 ? 4 * t + 2 * e : 2 * t + 8 * e));
+        float back = 1.f;
+        if constexpr (e4m3) {  // f16 of q 2^-x, x from the row's largest finite exponent
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t w = qf[k][n][e], lo = (w >> 7) & 0xffu, hi = (w >> 23) & 0xffu;
+                    top = max(top, max(lo < 255u ? lo : 0u, hi < 255u ? hi : 0u));
+                }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int x = min(max((int)top - 127 - 13, -120), 120);
+            const float f = __uint_as_float((uint32_t)(127 - x) << 23);
+            back = __uint_as_float((uint32_t)(127 + x) << 23);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t w = qf[k][n][e];
+                    qf[k][n][e] = pack_f16x2(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f);
+                }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int row = 2 * t + x + 8 * n;
+            cq[n][x] = p.scale * kLog2e * __shfl_sync(0xffffffffu, back, 4 * (2 * t + x));
+            pos[n][x] = row < rows ? first + (r0 + row) / p.G : -1;
+        }
+    }
+
+    // m: reference of the sums l, wm: of the outputs o (the same without a scale of values); log2.  All of a
+    // column's lanes hold the same references, each its own keys' share of the sum.
+    float o[D / 16][NQ][4], m[NQ][2], wm[NQ][2], l[NQ][2];
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][n][e] = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            m[n][x] = wm[n][x] = -INFINITY;
+            l[n][x] = 0.f;
+        }
+    }
+    const int edge = min(ke, low + 1);  // keys below it are seen by every row, but for a window
     for (int i = 0; i < mine; ++i) {
         asm volatile("cp.async.wait_group %0;" ::"n"(C::ST - 2) : "memory");
         __syncwarp();
         load(i + C::ST - 1);
         const uint32_t sk = smem_u32(ring + (i % C::ST) * C::STAGE), sv = sk + C::TILE;
-        float s[2][4] = {};
-        if constexpr (!e4m3) {
+        float s[KT][NQ][4] = {};
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                // matrices: keys 0-7 / 8-15 (lane bit 4) x channels 16k .. +7 / +8 .. +15 (lane bit 3)
-                uint32_t b[4];
-                ldm4(b, sk + chunk<C::ROW>((lane & 7) + (lane & 16) / 2, 2 * k + ((lane >> 3) & 1)));
-                mma_bf16(s[0], qf[k], b[0], b[1]);
-                mma_bf16(s[1], qf[k], b[2], b[3]);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < D / 16; k += 2) {
-                // keys 0-7 / 8-15 (lane bit 3) x 16 channels of step k / k + 1 (lane bit 4): a lane
-                // gets channels 4t .. 4t + 3 of key g
-                uint32_t b[4], x, y;
-                ldm4(b, sk + chunk<C::ROW>((lane & 7) + (lane & 8), k + (lane >> 4)));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    e4m3x4_f16(b[e], x, y);
-                    mma_f16(s[e & 1], qf[k + (e >> 1)], x, y);
-                }
-            }
-        }
-        const float *sc = reinterpret_cast<const float *>(ring + (i % C::ST) * C::STAGE + 2 * C::TILE);
-        const int k0 = kb + kStep * (warp + kWarps * i) + 2 * t;
-        // top: the largest score; wtop: the largest log2 weight (e4m3: with the value's scale)
-        float top[2] = {m[0], m[1]}, wtop[2] = {wm[0], wm[1]}, lv[2][2];
-        if constexpr (e4m3) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) lv[n][e] = __log2f(sc[kStep + 8 * n + 2 * t + e]);
-        }
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int key = k0 + 8 * n + (e & 1), x = e >> 1;
-                if constexpr (e4m3) s[n][e] *= sc[8 * n + 2 * t + (e & 1)] * qscale[x];
-                s[n][e] *= c;
-                const bool vis = key <= pos[x] && key < ke && (p.window == 0 || key > pos[x] - p.window);
-                s[n][e] = vis ? s[n][e] : -INFINITY;
-                top[x] = fmaxf(top[x], s[n][e]);
-                if constexpr (e4m3) wtop[x] = fmaxf(wtop[x], s[n][e] + lv[n][e & 1]);
-            }
-        bool grow[2], wgrow[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
-            grow[x] = top[x] - m[x] > kGrow;  // true for the row's first visible key (m = -inf)
-            wgrow[x] = grow[x];
-            if constexpr (e4m3) {
-                wtop[x] = fmaxf(wtop[x], __shfl_xor_sync(0xffffffffu, wtop[x], 1));
-                wtop[x] = fmaxf(wtop[x], __shfl_xor_sync(0xffffffffu, wtop[x], 2));
-                wgrow[x] = wtop[x] - wm[x] > kGrow;
-            } else {
-                wtop[x] = top[x];
-            }
-        }
-        if (__any_sync(0xffffffffu, grow[0] || grow[1] || wgrow[0] || wgrow[1])) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (grow[x]) {
-                    l[x] *= ex2(m[x] - top[x]);
-                    m[x] = top[x];
-                }
-                const float f = wgrow[x] ? ex2(wm[x] - wtop[x]) : 1.f;
-                if (wgrow[x]) wm[x] = wtop[x];
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    o[n][2 * x] *= f;
-                    o[n][2 * x + 1] *= f;
-                }
-            }
-        }
-        uint32_t pf[4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float off = m[x] == -INFINITY ? 0.f : m[x];  // no key visible yet: all weights 0
-                float a = ex2(s[n][2 * x] - off), b = ex2(s[n][2 * x + 1] - off);
-                l[x] += a + b;
-                if constexpr (e4m3) {
-                    const float woff = wm[x] == -INFINITY ? 0.f : wm[x] - kWeight;
-                    a = ex2(s[n][2 * x] + lv[n][0] - woff);
-                    b = ex2(s[n][2 * x + 1] + lv[n][1] - woff);
-                    pf[x + 2 * n] = pack_f16x2(a, b);
-                } else {
-                    pf[x + 2 * n] = pack_bf16x2(a, b);
-                }
-            }
-#pragma unroll
-        for (int d = 0; d < D / 16; d += (e4m3 ? 2 : 1)) {
+        for (int k = 0; k < D / 16; ++k) {
             uint32_t b[4];
             if constexpr (!e4m3) {
-                // keys 0-7 / 8-15 (lane bit 3) x 8 channels 2d / 2d + 1 (lane bit 4), transposed
-                ldm4t(b, sv + chunk<C::ROW>((lane & 7) + (lane & 8), 2 * d + (lane >> 4)));
-                mma_bf16(o[2 * d], pf, b[0], b[1]);
-                mma_bf16(o[2 * d + 1], pf, b[2], b[3]);
-            } else {
-                // 16 channels d / d + 1 in pairs of bytes: a lane gets channels 2g and 2g + 1 of keys
-                // 2t and 2t + 1, so output tile 2d holds the even channels of 16d .. and 2d + 1 the odd
-                ldm4t(b, sv + chunk<C::ROW>((lane & 7) + (lane & 8), d + (lane >> 4)));
-                uint32_t ev[4], od[4];
+                // matrices: keys 0-7 / 8-15 (lane bit 3) x channels 16k .. +7 / +8 .. +15 (lane bit 4)
+                ldm4(b, sk + chunk<C::ROW>((lane & 7) + (lane & 8), 2 * k + (lane >> 4)));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) e4m3x4_f16(__byte_perm(b[e], 0, 0x3120), ev[e], od[e]);
-                mma_f16(o[2 * d], pf, ev[0], ev[1]);
-                mma_f16(o[2 * d + 1], pf, od[0], od[1]);
-                mma_f16(o[2 * d + 2], pf, ev[2], ev[3]);
-                mma_f16(o[2 * d + 3], pf, od[2], od[3]);
+                for (int n = 0; n < NQ; ++n) mma_bf16(s[0][n], b, qf[k][n][0], qf[k][n][1]);
+            } else {
+                // keys 0-7 .. 24-31 (lane / 8) x the 16 channels of step k: a lane gets channels 4t .. 4t + 3
+                // of keys g, g + 8, ..
+                ldm4(b, sk + chunk<C::ROW>(lane, k));
+#pragma unroll
+                for (int h = 0; h < KT; ++h) {
+                    uint32_t a[4];
+                    e4m3x4_f16(b[2 * h], a[0], a[2]);
+                    e4m3x4_f16(b[2 * h + 1], a[1], a[3]);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) mma_f16(s[h][n], a, qf[k][n][0], qf[k][n][1]);
+                }
+            }
+        }
+        // s[h][n][e]: key 16 h + g + 8 (e / 2), query 8 n + 2t + e % 2
+        const float *sc = reinterpret_cast<const float *>(ring + (i % C::ST) * C::STAGE + 2 * C::TILE);
+        float lv[KT][2];  // log2 of the values' scales
+#pragma unroll
+        for (int h = 0; h < KT; ++h)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                float f = 1.f;
+                if constexpr (e4m3) {
+                    f = sc[16 * h + 8 * y + g];
+                    lv[h][y] = __log2f(sc[kStep + 16 * h + 8 * y + g]);
+                }
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) s[h][n][2 * y + x] *= e4m3 ? f * cq[n][x] : cq[n][x];
+            }
+        // only the steps at the part's ends, the newest keys and a window's edge hide a key from a row
+        const int kstep = kb + kStep * (warp + kWarps * i);
+        if (kstep + kStep > edge || (p.window && kstep <= high - p.window)) {
+#pragma unroll
+            for (int h = 0; h < KT; ++h)
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = kstep + 16 * h + g + 8 * (e >> 1), row = pos[n][e & 1];
+                        const bool vis = key <= row && key < ke && (p.window == 0 || key > row - p.window);
+                        s[h][n][e] = vis ? s[h][n][e] : -INFINITY;
+                    }
+        }
+        bool move = false, grow[NQ][2], wgrow[NQ][2];
+        float top[NQ][2], wtop[NQ][2];  // the largest score; the largest log2 weight (e4m3: with the value's scale)
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float a = m[n][x], w = wm[n][x];
+#pragma unroll
+                for (int h = 0; h < KT; ++h)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        a = fmaxf(a, s[h][n][2 * y + x]);
+                        if constexpr (e4m3) w = fmaxf(w, s[h][n][2 * y + x] + lv[h][y]);
+                    }
+#pragma unroll
+                for (int z = 4; z < 32; z <<= 1) {
+                    a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, z));
+                    if constexpr (e4m3) w = fmaxf(w, __shfl_xor_sync(0xffffffffu, w, z));
+                }
+                top[n][x] = a;
+                wtop[n][x] = e4m3 ? w : a;
+                grow[n][x] = a - m[n][x] > kGrow;  // true for the row's first visible key (m = -inf)
+                wgrow[n][x] = e4m3 ? w - wm[n][x] > kGrow : grow[n][x];
+                move |= grow[n][x] || wgrow[n][x];
+            }
+        if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (grow[n][x]) {
+                        l[n][x] *= ex2(m[n][x] - top[n][x]);
+                        m[n][x] = top[n][x];
+                    }
+                    const float f = wgrow[n][x] ? ex2(wm[n][x] - wtop[n][x]) : 1.f;
+                    if (wgrow[n][x]) wm[n][x] = wtop[n][x];
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d) {
+                        o[d][n][x] *= f;
+                        o[d][n][2 + x] *= f;
+                    }
+                }
+        }
+        uint32_t pf[KT][NQ][2];
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+            float off[2], woff[2];  // no key visible yet: all weights 0
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                off[x] = m[n][x] == -INFINITY ? 0.f : m[n][x];
+                woff[x] = wm[n][x] == -INFINITY ? 0.f : wm[n][x] - kWeight;
+            }
+#pragma unroll
+            for (int h = 0; h < KT; ++h)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    float a = ex2(s[h][n][2 * y] - off[0]), b = ex2(s[h][n][2 * y + 1] - off[1]);
+                    l[n][0] += a;
+                    l[n][1] += b;
+                    if constexpr (e4m3) {
+                        a = ex2(s[h][n][2 * y] + lv[h][y] - woff[0]);
+                        b = ex2(s[h][n][2 * y + 1] + lv[h][y] - woff[1]);
+                        pf[h][n][y] = transpose(pack_f16x2(a, b));
+                    } else {
+                        pf[h][n][y] = transpose(pack_bf16x2(a, b));
+                    }
+                }
+        }
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+            uint32_t b[4];
+            if constexpr (!e4m3) {
+                // keys 0-7 / 8-15 (lane bit 4) x channels 16d .. +7 / +8 .. +15 (lane bit 3), transposed
+                ldm4t(b, sv + chunk<C::ROW>((lane & 7) + ((lane >> 1) & 8), 2 * d + ((lane >> 3) & 1)));
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) mma_bf16(o[d][n], b, pf[0][n][0], pf[0][n][1]);
+            } else {
+                // keys 0-7 .. 24-31 x 16 channels 16d .. in pairs of bytes: a lane gets channels 2g and 2g + 1 of
+                // keys 2t and 2t + 1 (+ 8, ..), so rows 0-7 of the output tile are the even channels, 8-15 the odd
+                ldm4t(b, sv + chunk<C::ROW>(lane, d));
+#pragma unroll
+                for (int h = 0; h < KT; ++h) {
+                    uint32_t a[4];
+                    e4m3x4_f16(__byte_perm(b[2 * h], 0, 0x3120), a[0], a[1]);
+                    e4m3x4_f16(__byte_perm(b[2 * h + 1], 0, 0x3120), a[2], a[3]);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) mma_f16(o[d][n], a, pf[h][n][0], pf[h][n][1]);
+                }
             }
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-    }
     // ---- the warps' sums joined: O and (m, l) of each warp over the rings
     __syncthreads();
     float *so = reinterpret_cast<float *>(sm);
     __shared__ float s_m[kWarps][kRows], s_w[kWarps][kRows], s_l[kWarps][kRows];
     constexpr int OS = D + 4;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        float *dst = so + (warp * kRows + g + 8 * x) * OS;
+    for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int d = 0; d < D / 16; ++d) {
-            if constexpr (!e4m3) {
-                *reinterpret_cast<float2 *>(dst + 16 * d + 2 * t) = make_float2(o[2 * d][2 * x], o[2 * d][2 * x + 1]);
-                *reinterpret_cast<float2 *>(dst + 16 * d + 8 + 2 * t) = make_float2(o[2 * d + 1][2 * x], o[2 * d + 1][2 * x + 1]);
-            } else {
-                *reinterpret_cast<float4 *>(dst + 16 * d + 4 * t) =
-                    make_float4(o[2 * d][2 * x], o[2 * d + 1][2 * x], o[2 * d][2 * x + 1], o[2 * d + 1][2 * x + 1]);
+        for (int x = 0; x < 2; ++x) {
+            const int row = 8 * n + 2 * t + x;
+            float *dst = so + (warp * kRows + row) * OS;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                if constexpr (e4m3) {
+                    *reinterpret_cast<float2 *>(dst + 16 * d + 2 * g) = make_float2(o[d][n][x], o[d][n][2 + x]);
+                } else {
+                    dst[16 * d + g] = o[d][n][x];
+                    dst[16 * d + 8 + g] = o[d][n][2 + x];
+                }
+            }
+            float sum = l[n][x];
+#pragma unroll
+            for (int z = 4; z < 32; z <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, z);
+            if (g == 0) {
+                s_m[warp][row] = m[n][x];
+                s_w[warp][row] = e4m3 ? wm[n][x] - kWeight : m[n][x];
+                s_l[warp][row] = sum;
             }
         }
-        if (t == 0) {
-            s_m[warp][g + 8 * x] = m[x];
-            s_w[warp][g + 8 * x] = e4m3 ? wm[x] - kWeight : m[x];
-            s_l[warp][g + 8 * x] = l[x];
-        }
-    }
     __syncthreads();
     for (int i = tid; i < rows * (D / 4); i += kWarps * 32) {
         const int row = i / (D / 4), ch = i % (D / 4) * 4;
@@ -516,13 +590,19 @@ template <int D, int W> __global__ void __launch_bounds__(256) attn_join_kernel(
     if (p.lse && lane == 0) p.lse[at] = any ? top + __log2f(sum) * kLn2 : -INFINITY;
 }
 
-template <int D, bool e4m3> cudaError_t run(const Params &p, dim3 grid, cudaStream_t s)
+template <int D, bool e4m3, int NQ> cudaError_t run(const Params &p, dim3 grid, cudaStream_t s)
 {
-    auto kernel = attn_rows_kernel<D, e4m3>;
-    cudaError_t e = set_smem_attr(reinterpret_cast<const void *>(kernel), Cfg<D, e4m3>::SMEM);
+    auto kernel = attn_rows_kernel<D, e4m3, NQ>;
+    using C = Cfg<D, e4m3, NQ>;
+    cudaError_t e = set_smem_attr(reinterpret_cast<const void *>(kernel), C::SMEM);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kWarps * 32, Cfg<D, e4m3>::SMEM, s>>>(p);
+    kernel<<<grid, kWarps * 32, C::SMEM, s>>>(p);
     return cudaGetLastError();
+}
+template <int NQ> cudaError_t run(int D, bool e4m3, const Params &p, dim3 grid, cudaStream_t s)
+{
+    if (e4m3) return D == 128 ? run<128, true, NQ>(p, grid, s) : run<64, true, NQ>(p, grid, s);
+    return D == 128 ? run<128, false, NQ>(p, grid, s) : run<64, false, NQ>(p, grid, s);
 }
 
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
@@ -578,14 +658,15 @@ cudaError_t launch_attn_cached(const CachedArgs &a, bool use_tc, cudaStream_t s)
     if (use_tc) {
         e = launch_attn_cached_tc(a, s);
     } else {
+        const bool wide = a.b.rows * p.G > 8LL * a.b.n;  // more than 8 rows a sequence, on average
+        const int rows = wide ? 16 : 8;
         long long keys = (long long)a.c.width * a.c.page;
-        if (a.window > 0 && a.window + kRows < keys) keys = a.window + kRows;
-        p.piece = ceil_div(ceil_div(keys, a.splits), kStep * kWarps) * kStep * kWarps;
-        const long long tiles = a.b.n + a.b.rows * p.G / kRows;
+        if (a.window > 0 && a.window + rows < keys) keys = a.window + rows;
+        p.piece = ceil_div(ceil_div(keys, a.splits), 128) * 128;  // whole steps of the four warps
+        const long long tiles = a.b.n + a.b.rows * p.G / rows;
         if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
         const dim3 grid((unsigned)tiles, (unsigned)a.Hkv, (unsigned)a.splits);
-        if (a.c.e4m3) e = a.D == 128 ? run<128, true>(p, grid, s) : run<64, true>(p, grid, s);
-        else e = a.D == 128 ? run<128, false>(p, grid, s) : run<64, false>(p, grid, s);
+        e = wide ? run<2>(a.D, a.c.e4m3, p, grid, s) : run<1>(a.D, a.c.e4m3, p, grid, s);
     }
     if (e != cudaSuccess || a.splits == 1) return e;
     const long long rows = a.b.rows * a.H;
