@@ -27,16 +27,24 @@ def _bytes(t):
 
 
 def _need(name, t, dtype, shape, dev):
-    """`t` is a contiguous tensor of this dtype, shape (a tuple; None: any) and device, or None."""
-    if t is None or (t.dtype is dtype and t.device == dev and (shape is None or t.shape == shape) and t.is_contiguous()):
+    """`t` is a contiguous tensor of this dtype, shape (a tuple; None: any) and device, or None.  One
+    expression on the way of every call; what is wrong is found out afterwards."""
+    if t is None or (t.dtype is dtype and t.get_device() == dev and (shape is None or t.shape == shape) and t.is_contiguous()):
         return
-    if t.device != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on {dev}, is on {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the call's device, is on {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
     raise ValueError(f"{name} must be contiguous")
+
+
+def _device(t):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"the tensors must be CUDA tensors, are on {t.device}")
+    return dev
 
 
 @contextlib.contextmanager
@@ -50,23 +58,21 @@ _HERE = contextlib.nullcontext()
 
 def _on(dev, stream):
     """The device and stream of a call, for its allocations and its launches."""
-    if dev.type != "cuda":
-        raise ValueError(f"the tensors must be CUDA tensors, are on {dev}")
-    if stream is None and dev.index == torch.cuda.current_device():
+    if stream is None and dev == torch.cuda.current_device():
         return _HERE
     return _elsewhere(dev, torch.cuda.current_stream(dev) if stream is None else stream)
 
 
 def _current(dev):
     # the handle alone: torch.cuda.current_stream() builds a Stream object, 3 us of a decode step's call
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _workspace(ws, nbytes, dev):
     if ws is None and nbytes > 0:
         return torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if ws is not None and ws.device != dev:
-        raise ValueError(f"workspace must be on {dev}")
+    if ws is not None and ws.get_device() != dev:
+        raise ValueError("workspace must be on the call's device")
     return ws
 
 
@@ -76,7 +82,7 @@ def _scale(scale, D):
 
 # ------------------------------------------------------------------ norm and rotation
 def _rope_args(q, k, q_weight, k_weight, positions, inv_freq):
-    dev, dtype, qs, ks = q.device, q.dtype, q.shape, k.shape
+    dev, dtype, qs, ks = _device(q), q.dtype, q.shape, k.shape
     if len(qs) < 2 or len(ks) != len(qs) or ks[:-2] != qs[:-2] or ks[-1] != qs[-1]:
         raise ValueError("q and k are [.., H, D] and [.., Hkv, D] over the same rows")
     H, D = qs[-2:]
@@ -134,7 +140,7 @@ def gdn2_qk_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, d_q_out, d_k
             _need("dq_weight", out["dq_weight"], torch.float32, (D,), dev)
             _need("dk_weight", out["dk_weight"], torch.float32, (D,), dev)
         if norm and (out["dq_weight"] is not None or out["dk_weight"] is not None):
-            workspace = _workspace(workspace, int(raw().gdn2_qk_rope_workspace_size(flags, _dt(q), N, H, Hkv, D)), dev)
+            workspace = _workspace(workspace, raw().gdn2_qk_rope_workspace_size(flags, _dt(q), N, H, Hkv, D), dev)
         st = raw().gdn2_qk_rope_bwd(flags, _dt(q), N, H, Hkv, D, rot, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
                                     _ptr(positions), _ptr(inv_freq), eps, rot_scale, _ptr(d_q_out), _ptr(d_k_out),
                                     _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dq_weight"]), _ptr(out["dk_weight"]),
@@ -145,7 +151,7 @@ def gdn2_qk_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, d_q_out, d_k
 
 # ------------------------------------------------------------------ attention over whole sequences
 def _attn_args(q, k, v, cu_seqlens):
-    dev, dtype, qs, ks = q.device, q.dtype, q.shape, k.shape
+    dev, dtype, qs, ks = _device(q), q.dtype, q.shape, k.shape
     packed = cu_seqlens is not None
     if len(qs) != (3 if packed else 4) or len(ks) != len(qs):
         raise ValueError("q and k, v are " + ("[total_T, H, D] and [total_T, Hkv, D]" if packed else
@@ -209,7 +215,7 @@ def _attn_bwd(q, k, v, o, lse, d_o, cu_seqlens, window, scale, out, workspace, s
             for name, x in (("dq", q), ("dk", k), ("dv", v)):
                 _need(name, out[name], dtype, x.shape, dev)
         rows = t if cu_seqlens is not None else n * t
-        workspace = _workspace(workspace, int(raw().gdn2_attn_workspace_size(_dt(q), 1, rows, H, Hkv, D)), dev)
+        workspace = _workspace(workspace, raw().gdn2_attn_workspace_size(_dt(q), 1, rows, H, Hkv, D), dev)
         head = (_dt(q), n, t, H, Hkv, D, window, _scale(scale, D))
         tail = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(d_o), _ptr(out["dq"]), _ptr(out["dk"]),
                 _ptr(out["dv"]), _ptr(workspace), _bytes(workspace), _current(dev))
@@ -241,7 +247,7 @@ def gdn2_attn_workspace_size(dtype, N: int, T: int, H: int, Hkv: int, D: int) ->
 
 # ------------------------------------------------------------------ the paged cache
 def _cache_args(k_cache, v_cache, cu_seqlens, kv_lens, block_table, k_scale, v_scale):
-    dev, dtype, shape = k_cache.device, k_cache.dtype, k_cache.shape
+    dev, dtype, shape = _device(k_cache), k_cache.dtype, k_cache.shape
     if len(shape) != 4 or block_table.dim() != 2:
         raise ValueError("k_cache and v_cache are [num_pages, page_size, Hkv, D], block_table is [N, max_pages]")
     if dtype is torch.bfloat16:
@@ -327,8 +333,10 @@ def gdn2_attn_cached(q, k_cache, v_cache, cu_seqlens, kv_lens, block_table, k_sc
         elif want_lse:
             lse = torch.empty(T, H, dtype=torch.float32, device=dev)
         if workspace is None:
-            workspace = _workspace(None, gdn2_attn_cached_workspace_size(N, T, H, Hkv, D, window, sizes[0], sizes[2]),
-                                   dev)
+            workspace = _workspace(None, raw().gdn2_attn_cached_workspace_size(GDN2_BF16, N, T, H, Hkv, D, window,
+                                                                               sizes[0], sizes[2]), dev)
+        else:
+            _workspace(workspace, 0, dev)
         st = raw().gdn2_attn_cached(kind, GDN2_BF16, N, T, H, Hkv, D, window, _scale(scale, D), _ptr(cu_seqlens),
                                     _ptr(kv_lens), _ptr(block_table), *sizes, _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                     _ptr(k_scale), _ptr(v_scale), _ptr(o), _ptr(lse), _ptr(workspace),

@@ -622,7 +622,7 @@ CachedPlan cached_plan(int n, long long rows, int H, int Hkv, int window, long l
         plan.splits = (int)(want < keys / 512 ? want : keys / 512);
     } else {
         const long long blocks = (long long)n * Hkv;
-        long long want = ceil_div(4LL * device_sms(), blocks);
+        long long want = ceil_div(2LL * device_sms(), blocks);
         const long long even = ceil_div(keys, 2048);  // ragged lengths: no block reads more than 2048 keys
         if (want < even) want = even;
         plan.splits = (int)(want < keys / 256 ? want : keys / 256);

@@ -10,9 +10,11 @@
 //
 // Both are bound by memory: x is read and y written once (backward: x and dy read, dx written).
 // A warp owns a token and walks over its heads, as many lanes to a row as it has 16-byte vectors
-// (bf16: 16 for D = 128, 8 for D = 64; fp32: twice that), so that the token's cosines and sines
-// stay in registers for all of its heads.  The angle is formed and reduced modulo 2 pi in 64
-// bits: pos * inv_freq in fp32 would be off by 2^-24 of an angle of up to 10^5.
+// (bf16: 16 for D = 128, 8 for D = 64; fp32: twice that), four rows' loads in flight to a lane, so that
+// the token's cosines and sines stay in registers for all of its heads.  They are multiplied by the
+// weights first, and the partner channel comes as it was loaded: y_e = r (x_e (c_e w_e) + x_p (s_e w_p)).
+// The angle is formed and reduced modulo 2 pi in 64 bits: pos * inv_freq in fp32 would be off by
+// 2^-24 of an angle of up to 10^5.
 #include "attn.cuh"
 
 namespace gdn2 {
@@ -21,37 +23,43 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kShareBelow = 2048;  // tokens
 
-template <typename T> struct Vec;
-template <> struct Vec<float> { static constexpr int n = 4; };
-template <> struct Vec<__nv_bfloat16> { static constexpr int n = 8; };
+template <typename T> constexpr int kVec = 16 / sizeof(T);  // elements of a 16-byte vector
 
-template <typename T> __device__ __forceinline__ uint4 load_raw(const T *p) { return *reinterpret_cast<const uint4 *>(p); }
-__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[4])
+// V elements as V / 2 pairs of fp32
+__device__ __forceinline__ void unpack(const uint4 &v, uint64_t (&f)[2])
 {
-    f[0] = __uint_as_float(v.x);
-    f[1] = __uint_as_float(v.y);
-    f[2] = __uint_as_float(v.z);
-    f[3] = __uint_as_float(v.w);
+    f[0] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+    f[1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
 }
-__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[8])
+__device__ __forceinline__ void unpack(const uint4 &v, uint64_t (&f)[4])
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i) f[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
-__device__ __forceinline__ void store_vec(float *p, const float (&f)[4])
+__device__ __forceinline__ uint4 pack(const uint64_t (&f)[2])
 {
-    *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    float a, b, c, d;
+    unpair(f[0], a, b);
+    unpair(f[1], c, d);
+    return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
 }
-__device__ __forceinline__ void store_vec(__nv_bfloat16 *p, const float (&f)[8])
+__device__ __forceinline__ uint4 pack(const uint64_t (&f)[4])
 {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        unpair(f[i], a, b);
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(b), "f"(a));
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ float sum_of(uint64_t x)
+{
+    float a, b;
+    unpair(x, a, b);
+    return a + b;
 }
 
 // cos and sin of pos * inv, times f.  The product of an int and a float is exact in 64 bits, and so
@@ -72,87 +80,87 @@ __device__ __forceinline__ void angle(int pos, float inv, float f, float &c, flo
 // that ends inside a vector, exchanged through shared memory.
 enum { kPair, kSwap, kAny };
 
-// Rotates this lane's vector f (channels ch .. ch + V - 1 of its row) in place; the backward's
-// transpose comes as negated sines.
-template <int V, int mode>
-__device__ __forceinline__ void rotate(float (&f)[V], const float (&c)[V], const float (&s)[V], int ch, int rot,
-                                       float *buf, int lane)
+// the channel that channel i is rotated with (itself past rot)
+template <int mode> __device__ __forceinline__ int partner(int i, int rot)
 {
+    if (i >= rot) return i;
+    return mode == kPair ? i ^ 1 : i < (rot >> 1) ? i + (rot >> 1) : i - (rot >> 1);
+}
+// The partners of this lane's channels ch .. ch + V - 1, of vector x as it was loaded.  buf: kAny's
+// buffer of this lane's row.
+template <typename T, int mode>
+__device__ __forceinline__ uint4 partners(const uint4 &x, int ch, int rot, T *buf, int lane)
+{
+    constexpr int V = kVec<T>;
     if constexpr (mode == kPair) {
+        if (ch >= rot) return x;
+        uint4 y;
+        if constexpr (V == 8) y = make_uint4(__byte_perm(x.x, 0, 0x1032), __byte_perm(x.y, 0, 0x1032), __byte_perm(x.z, 0, 0x1032), __byte_perm(x.w, 0, 0x1032));
+        else y = make_uint4(x.y, x.x, x.w, x.z);
+        if (ch + V > rot) {  // the rotated part ends inside the vector, after whole pairs
+            uint32_t *ys = reinterpret_cast<uint32_t *>(&y);
+            const uint32_t *xs = reinterpret_cast<const uint32_t *>(&x);
 #pragma unroll
-        for (int e = 0; e < V; e += 2) {
-            const float a = f[e], b = f[e + 1];
-            f[e] = a * c[e] - b * s[e];
-            f[e + 1] = b * c[e] + a * s[e];
+            for (int e = 0; e < 4; ++e)
+                if (ch + e * (V / 4) >= rot) ys[e] = xs[e];
         }
+        return y;
+    } else if constexpr (mode == kSwap) {
+        const int step = (rot >> 1) / V;  // lanes between a channel and its partner
+        const int src = ch >= rot ? lane : ch < (rot >> 1) ? lane + step : lane - step;
+        return make_uint4(__shfl_sync(0xffffffffu, x.x, src), __shfl_sync(0xffffffffu, x.y, src),
+                          __shfl_sync(0xffffffffu, x.z, src), __shfl_sync(0xffffffffu, x.w, src));
     } else {
-        // c = 1, s = 0 past rot; s is negative in the lower half
-        const int half = rot >> 1;
-        float o[V];
-        if constexpr (mode == kSwap) {
-            const int step = half / V;  // lanes between a channel and its partner
-            const int src = ch < half ? lane + step : lane - step;
+        __syncwarp();
+        *reinterpret_cast<uint4 *>(buf + ch) = x;
+        __syncwarp();
+        uint4 y;
+        T *ys = reinterpret_cast<T *>(&y);
 #pragma unroll
-            for (int e = 0; e < V; ++e) o[e] = __shfl_sync(0xffffffffu, f[e], src & 31);
-        } else {
-            // row buffer of the lanes that share this row: channel ch + e at buf[ch + e]
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < V; ++e) buf[ch + e] = f[e];
-            __syncwarp();
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const int i = ch + e;
-                o[e] = i < half ? buf[i + half] : i < rot ? buf[i - half] : 0.f;
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) f[e] = f[e] * c[e] + (s[e] != 0.f ? o[e] * s[e] : 0.f);
+        for (int e = 0; e < V; ++e) ys[e] = buf[partner<mode>(ch + e, rot)];
+        return y;
     }
 }
 
 template <typename T, int D, int mode, bool bwd>
-__global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeArgs a)
+__global__ void __launch_bounds__(kWarps * 32, bwd ? 2 : 3) rope_kernel(const RopeArgs a)
 {
-    constexpr int V = Vec<T>::n, L = D / V, R = 32 / L;  // elements per lane, lanes per row, rows per warp pass
-    constexpr int U = bwd ? 2 : 4;                       // passes whose loads are in flight together
-    __shared__ float sbuf[mode == kAny ? kWarps * R * D : 1];
+    constexpr int V = kVec<T>, P = V / 2, L = D / V, R = 32 / L;  // elements and pairs per lane, lanes per row, rows per pass
+    constexpr int U = 4;                                           // passes whose loads are in flight together
+    __shared__ __align__(16) T sbuf[mode == kAny ? kWarps * R * D : 8];
     __shared__ float2 scs[kWarps][D / 2];
-    __shared__ float sw[bwd ? kWarps * R : 1][bwd ? D : 1];
+    __shared__ uint64_t sdw[bwd ? 2 : 1][bwd ? kWarps : 1][bwd ? P : 1][32];  // weight gradients, a lane's own sums
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int ch = (lane % L) * V, sub = lane / L, half = a.rot >> 1;
-    float *buf = sbuf + (mode == kAny ? (warp * R + sub) * D : 0);
-    float wt[2][V], dw[2][V];
+    T *buf = sbuf + (mode == kAny ? (warp * R + sub) * D : 0);
+    if constexpr (bwd) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        wt[0][e] = a.norm && a.wq ? a.wq[ch + e] : 1.f;
-        wt[1][e] = a.norm && a.wk ? a.wk[ch + e] : 1.f;
-        dw[0][e] = dw[1][e] = 0.f;
+        for (int e = 0; e < P; ++e) sdw[0][warp][e][lane] = sdw[1][warp][e][lane] = 0;
     }
     // Few tokens: the warps of a block share one token's heads (a decode step then fills the SMs);
     // many: a warp to a token, whose angles are formed once.
-    const int share = a.n < kShareBelow ? kWarps : 1, heads = a.H + a.Hkv;
+    const int share = a.n < kShareBelow ? kWarps : 1;
     const int first = share == 1 ? 0 : warp * R, step = share == 1 ? R : kWarps * R;
     const long long per = kWarps / share;
     for (long long t0 = (long long)blockIdx.x * per; t0 < a.n; t0 += (long long)gridDim.x * per) {
         const long long t = t0 + (share == 1 ? warp : 0);
         if (t >= a.n) break;
         const int pos = a.rot ? a.pos[t] : 0;
-        uint4 xr[U], gr[U];  // vectors of the next U passes, as loaded
-        auto fetch = [&](int h0) {
+        uint4 xr[U], gr[U];
+        auto fetch = [&](int isk, int h0) {
+            const int heads = isk ? a.Hkv : a.H;
+            const T *x = static_cast<const T *>(isk ? a.k : a.q) + (size_t)t * heads * D + ch;
+            const T *g = static_cast<const T *>(isk ? a.dko : a.dqo) + (size_t)t * heads * D + ch;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int h = h0 + u * step + sub;
                 xr[u] = gr[u] = make_uint4(0, 0, 0, 0);
-                if (h >= heads) continue;
-                const bool isk = h >= a.H;
-                const size_t off = ((size_t)t * (isk ? a.Hkv : a.H) + (isk ? h - a.H : h)) * D + ch;
-                if (!bwd || a.norm) xr[u] = load_raw(static_cast<const T *>(isk ? a.k : a.q) + off);
-                if (bwd) gr[u] = load_raw(static_cast<const T *>(isk ? a.dko : a.dqo) + off);
+                if (h < heads && (!bwd || a.norm)) xr[u] = *reinterpret_cast<const uint4 *>(x + (size_t)h * D);
+                if (bwd && h < heads) gr[u] = *reinterpret_cast<const uint4 *>(g + (size_t)h * D);
             }
         };
-        fetch(first);
-        // the token's angles, two or one to a lane
+        fetch(0, first);
+        // the token's angles, two or one to a lane, while the first rows come
         __syncwarp();
         for (int i = lane; i < half; i += 32) {
             float c, s;
@@ -160,87 +168,100 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeArgs a)
             scs[warp][i] = make_float2(c, bwd ? -s : s);
         }
         __syncwarp();
-        float c[V], s[V];
+#pragma unroll 1
+        for (int isk = 0; isk < 2; ++isk) {
+            const int heads = isk ? a.Hkv : a.H;
+            T *y = static_cast<T *>(bwd ? (isk ? a.dk : a.dq) : (isk ? a.ko : a.qo)) + (size_t)t * heads * D + ch;
+            const float *w = a.norm ? (isk ? a.wk : a.wq) : nullptr;
+            // own and partner's factors; forward: with the weights of the channels they multiply
+            uint64_t own[P], oth[P], wt[P], dw[P];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const int i = ch + e;
-            const int at = mode == kPair ? i >> 1 : i < half ? i : i - half;
-            const float2 cs = i < a.rot ? scs[warp][at] : make_float2(1.f, 0.f);
-            c[e] = cs.x;
-            s[e] = mode != kPair && i < half ? -cs.y : cs.y;
-        }
-        for (int h0 = first; h0 < heads; h0 += U * step) {
-            uint4 xn[U], gn[U];
+            for (int e = 0; e < P; ++e) {
+                float c[2], s[2], f[2];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                xn[u] = xr[u];
-                gn[u] = gr[u];
+                for (int z = 0; z < 2; ++z) {
+                    const int i = ch + 2 * e + z;
+                    const float2 cs = i < a.rot ? scs[warp][mode == kPair ? i >> 1 : i < half ? i : i - half] : make_float2(1.f, 0.f);
+                    f[z] = w ? w[i] : 1.f;
+                    c[z] = cs.x;
+                    s[z] = (mode == kPair ? !(i & 1) : i < half) ? -cs.y : cs.y;
+                    if (!bwd && w) {
+                        c[z] *= f[z];
+                        s[z] *= w[partner<mode>(i, a.rot)];
+                    }
+                }
+                own[e] = pair(c[0], c[1]);
+                oth[e] = pair(s[0], s[1]);
+                wt[e] = pair(f[0], f[1]);
+                dw[e] = 0;
             }
-            if (h0 + U * step < heads) fetch(h0 + U * step);
+            for (int h0 = first; h0 < heads; h0 += U * step) {
+                if (isk || h0 > first) fetch(isk, h0);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int h = h0 + u * step + sub;
-                if (h0 + u * step >= heads) break;  // the whole warp's pass
-                const bool live = h < heads, isk = h >= a.H;
-                const size_t off = ((size_t)t * (isk ? a.Hkv : a.H) + (live ? (isk ? h - a.H : h) : 0)) * D + ch;
-                float x[V], g[V];
-                unpack(xn[u], x);
-                if (bwd) unpack(gn[u], g);
-                float r = 1.f;
-                if (a.norm) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) ss += x[e] * x[e];
-#pragma unroll
-                    for (int m = L / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-                    r = rsqrtf(ss * (1.f / D) + a.eps);
-                }
-                if constexpr (!bwd) {
+                for (int u = 0; u < U; ++u) {
+                    const int h = h0 + u * step + sub;
+                    if (h0 + u * step >= heads) break;  // the whole warp's pass
+                    uint64_t f[P], o[P];
+                    unpack(xr[u], f);
+                    float r = 1.f;
                     if (a.norm) {
+                        uint64_t s2 = mul2(f[0], f[0]);
 #pragma unroll
-                        for (int e = 0; e < V; ++e) x[e] = x[e] * r * (isk ? wt[1][e] : wt[0][e]);
+                        for (int e = 1; e < P; ++e) s2 = fma2(f[e], f[e], s2);
+                        float ss = sum_of(s2);
+#pragma unroll
+                        for (int m = L / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
+                        r = rsqrtf(ss * (1.f / D) + a.eps);
                     }
-                    rotate<V, mode>(x, c, s, ch, a.rot, buf, lane);
-                    if (live) store_vec(static_cast<T *>(isk ? a.ko : a.qo) + off, x);
-                } else {
-                    rotate<V, mode>(g, c, s, ch, a.rot, buf, lane);
-                    if (a.norm) {
-                        float dot = 0.f;
+                    const uint64_t r2 = pair(r, r);
+                    if constexpr (!bwd) {
+                        unpack(partners<T, mode>(xr[u], ch, a.rot, buf, lane), o);
 #pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            x[e] *= r;  // the normalised row
-                            const float ux = g[e] * x[e];
-                            dw[0][e] += isk ? 0.f : ux;
-                            dw[1][e] += isk ? ux : 0.f;
-                            g[e] *= isk ? wt[1][e] : wt[0][e];
-                            dot += g[e] * x[e];
+                        for (int e = 0; e < P; ++e) f[e] = mul2(fma2(o[e], oth[e], mul2(f[e], own[e])), r2);
+                        if (h < heads) *reinterpret_cast<uint4 *>(y + (size_t)h * D) = pack(f);
+                    } else {
+                        uint64_t u2[P];
+                        unpack(gr[u], u2);
+                        unpack(partners<T, mode>(gr[u], ch, a.rot, buf, lane), o);
+                        uint64_t d2 = 0;
+#pragma unroll
+                        for (int e = 0; e < P; ++e) {
+                            u2[e] = fma2(o[e], oth[e], mul2(u2[e], own[e]));
+                            if (a.norm) {
+                                const uint64_t ux = mul2(u2[e], f[e]);
+                                dw[e] = fma2(ux, r2, dw[e]);
+                                d2 = fma2(ux, wt[e], d2);
+                            }
                         }
+                        if (a.norm) {  // dx = u (r w) - x (r^3 / D sum u w x)
+                            float dot = sum_of(d2);
 #pragma unroll
-                        for (int m = L / 2; m >= 1; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-                        dot *= 1.f / D;
+                            for (int m = L / 2; m >= 1; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+                            dot *= -r * r * r * (1.f / D);
+                            const uint64_t k2 = pair(dot, dot);
 #pragma unroll
-                        for (int e = 0; e < V; ++e) g[e] = r * (g[e] - x[e] * dot);
+                            for (int e = 0; e < P; ++e) u2[e] = fma2(u2[e], mul2(wt[e], r2), mul2(f[e], k2));
+                        }
+                        if (h < heads) *reinterpret_cast<uint4 *>(y + (size_t)h * D) = pack(u2);
                     }
-                    if (live) store_vec(static_cast<T *>(isk ? a.dk : a.dq) + off, g);
                 }
+            }
+            if constexpr (bwd) {
+#pragma unroll
+                for (int e = 0; e < P; ++e) sdw[isk][warp][e][lane] = add2(sdw[isk][warp][e][lane], dw[e]);
             }
         }
     }
     if constexpr (bwd) {
         if (!a.partial) return;
-        // the block's sums, over its warps in order, into its row of `partial` [2][blocks][D]
+        // the block's sums, over its warps and their rows of a pass in order, into its row of `partial` [2][blocks][D]
+        __syncthreads();
+        for (int i = threadIdx.x; i < D; i += kWarps * 32) {  // two channels of q or k
+            const int which = i / (D / 2), c = i - which * (D / 2);
+            uint64_t sum = 0;
 #pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            __syncthreads();
-#pragma unroll
-            for (int e = 0; e < V; ++e) sw[warp * R + sub][ch + e] = dw[which][e];
-            __syncthreads();
-            for (int i = threadIdx.x; i < D; i += kWarps * 32) {
-                float sum = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps * R; ++w) sum += sw[w][i];
-                a.partial[((size_t)which * gridDim.x + blockIdx.x) * D + i] = sum;
-            }
+            for (int w = 0; w < kWarps * R; ++w) sum = add2(sum, sdw[which][w / R][c % P][w % R * L + c / P]);
+            *reinterpret_cast<uint64_t *>(a.partial + ((size_t)which * gridDim.x + blockIdx.x) * D + 2 * c) = sum;
         }
     }
 }
@@ -262,10 +283,10 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float *partial, int
     if (threadIdx.x == 0 && dst) dst[blockIdx.x * 32 + threadIdx.y] = v;
 }
 
+// Many tokens: a few of them to a warp, six blocks to an SM (two or three run at a time).
 unsigned rope_grid(long long n)
 {
-    const long long want = n < kShareBelow ? n : (n + kWarps - 1) / kWarps;
-    const long long most = (long long)device_sms() * 4;
+    const long long want = n < kShareBelow ? n : (n + kWarps - 1) / kWarps, most = (long long)device_sms() * 6;
     return (unsigned)(want < most ? want : most);
 }
 
@@ -273,7 +294,7 @@ template <typename T, int D, bool bwd> void run(const RopeArgs &a, unsigned grid
 {
     const int half = a.rot >> 1;
     if (a.interleaved || a.rot == 0) rope_kernel<T, D, kPair, bwd><<<grid, kWarps * 32, 0, s>>>(a);
-    else if (half % Vec<T>::n == 0) rope_kernel<T, D, kSwap, bwd><<<grid, kWarps * 32, 0, s>>>(a);
+    else if (half % kVec<T> == 0) rope_kernel<T, D, kSwap, bwd><<<grid, kWarps * 32, 0, s>>>(a);
     else rope_kernel<T, D, kAny, bwd><<<grid, kWarps * 32, 0, s>>>(a);
 }
 
