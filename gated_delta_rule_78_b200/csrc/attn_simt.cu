@@ -5,34 +5,38 @@
 //   backward  p_ij = e^(s_ij - lse_i),  delta_i = do_i . o_i,  ds_ij = p_ij (do_i . v_j - delta_i)
 //             dv_j = sum_i p_ij do_i,  dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i
 //
-// 64 x 64 tiles, 256 threads, a 4 x 4 block of the scores to a thread; every product reads its two
-// operands from shared memory, the accumulators stay in registers.  Bound by the FP32 pipe and by
-// shared-memory loads (2 16-byte loads to 16 FMAs).  The backward runs two kernels, one to a query
-// tile (dq), one to a key tile (dk, dv, over all query heads of its key head), so that no sum
+// A block owns 32 queries, or for dk and dv 16 or 32 keys, and walks over the other side in tiles of 64.  Its
+// groups of 4 threads to a row take the tiles in turn, each with shared memory of its own, and add up at
+// the end, in order: an fp32 batch is mostly a small one, whose few blocks would otherwise leave an SM two
+// warps to a scheduler.  A thread forms 4 x 4 scores and 4 rows x D / 16 channels of each product, with
+// 16-byte loads of both operands from shared memory: 12 wavefronts of them to 64 FMAs of a warp, so
+// bound by the FP32 pipe first and shared memory next.  The backward runs two kernels, so that no sum
 // depends on the order in which blocks run.
 #include "attn.cuh"
 
 namespace gdn2 {
 namespace {
 
-constexpr int BT = 64, kThreads = 256;
+constexpr int BQ = 32, BC = 64;  // queries of a block (keys of one: 16 or 32), columns of a tile
 
-// shared-memory rows of D + 4 floats: 16-byte aligned, and 16 rows apart in different banks
+// shared-memory rows of D + 4 floats: 16-byte aligned, eight rows' 16 bytes in different banks
 template <int D> constexpr int kStride = D + 4;
-constexpr int kPs = BT + 4;
+constexpr int kPs = BC + 4;
 
-template <int D>
-__device__ __forceinline__ void load_tile(float *dst, const float *src, int rows, size_t stride)
+// rows [0, n) of a [n][D] tile (zeros from `rows` on), by the `threads` threads numbered tid
+template <int D, int n>
+__device__ __forceinline__ void load_tile(float *dst, const float *src, int rows, size_t stride, int tid, int threads)
 {
-    for (int i = threadIdx.x; i < BT * D / 4; i += kThreads) {
+    for (int i = tid; i < n * D / 4; i += threads) {
         const int r = i / (D / 4), c = i % (D / 4) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < rows) v = *reinterpret_cast<const float4 *>(src + (size_t)r * stride + c);
         *reinterpret_cast<float4 *>(dst + r * kStride<D> + c) = v;
     }
 }
+template <int n> __device__ __forceinline__ void group_sync(int group) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(n) : "memory"); }
 
-// acc[i][j] += A[ty + 16 i] . B[tx + 16 j] over D channels
+// acc[i][j] += A[4 ty + i] . B[tx + 16 j] over D channels
 template <int D>
 __device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float *A, const float *B, int ty, int tx)
 {
@@ -40,7 +44,7 @@ __device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float *A, con
     for (int c = 0; c < D; c += 4) {
         float4 x[4], y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(A + (ty + 16 * i) * kStride<D> + c);
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(A + (4 * ty + i) * kStride<D> + c);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * kStride<D> + c);
 #pragma unroll
@@ -55,27 +59,28 @@ __device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float *A, con
     }
 }
 
-// acc[i][n] += sum over the 64 rows t of P(ty + 16 i, t) * X[t][4 tx + (n & 3) + 64 (n / 4)]
-// P is row-major [64][kPs]; kT reads it transposed.
-template <int D, bool kT>
+// acc[i][n] += sum over the 64 columns t of P[4 ty + i][t] * X[t][64 (n / 4) + 4 tx + n % 4]
+template <int D>
 __device__ __forceinline__ void mul_tile(float (&acc)[4][D / 16], const float *P, const float *X, int ty, int tx)
 {
-#pragma unroll 4
-    for (int t = 0; t < BT; ++t) {
-        float p[4];
+#pragma unroll 2
+    for (int t = 0; t < BC; t += 4) {
+        float p[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = kT ? P[t * kPs + ty + 16 * i] : P[(ty + 16 * i) * kPs + t];
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<float4 *>(p[i]) = *reinterpret_cast<const float4 *>(P + (4 * ty + i) * kPs + t);
 #pragma unroll
-        for (int n = 0; n < D / 64; ++n) {
-            const float4 x = *reinterpret_cast<const float4 *>(X + t * kStride<D> + 64 * n + 4 * tx);
+        for (int z = 0; z < 4; ++z)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[i][4 * n] = fmaf(p[i], x.x, acc[i][4 * n]);
-                acc[i][4 * n + 1] = fmaf(p[i], x.y, acc[i][4 * n + 1]);
-                acc[i][4 * n + 2] = fmaf(p[i], x.z, acc[i][4 * n + 2]);
-                acc[i][4 * n + 3] = fmaf(p[i], x.w, acc[i][4 * n + 3]);
+            for (int n = 0; n < D / 64; ++n) {
+                const float4 x = *reinterpret_cast<const float4 *>(X + (t + z) * kStride<D> + 64 * n + 4 * tx);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[i][4 * n] = fmaf(p[i][z], x.x, acc[i][4 * n]);
+                    acc[i][4 * n + 1] = fmaf(p[i][z], x.y, acc[i][4 * n + 1]);
+                    acc[i][4 * n + 2] = fmaf(p[i][z], x.z, acc[i][4 * n + 2]);
+                    acc[i][4 * n + 3] = fmaf(p[i][z], x.w, acc[i][4 * n + 3]);
+                }
             }
-        }
     }
 }
 
@@ -83,50 +88,85 @@ __device__ __forceinline__ bool visible(int i, int j, int len, int window)
 {
     return j <= i && i < len && (window == 0 || i - j < window);
 }
-// first key tile that any of the queries from q0 on sees
-__device__ __forceinline__ int first_key_tile(int q0, int window)
+
+// This thread's 4 x D / 16 sums as a row-major [rows][D] tile, and the sum of the groups' tiles, group 0 first.
+// The caller's barriers lie between.
+template <int D> __device__ __forceinline__ void put_sums(float *dst, const float (&acc)[4][D / 16], int ty, int tx)
 {
-    return window == 0 || q0 < window ? 0 : (q0 - window + 1) / BT;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < D / 64; ++n)
+            *reinterpret_cast<float4 *>(dst + (4 * ty + i) * D + 64 * n + 4 * tx) =
+                make_float4(acc[i][4 * n], acc[i][4 * n + 1], acc[i][4 * n + 2], acc[i][4 * n + 3]);
+}
+template <int D, int BR, int NG>
+__device__ __forceinline__ void store_sums(float *out, size_t stride, const float *sums, size_t gap, float f, int rows)
+{
+    for (int i = threadIdx.x; i < BR * D / 4; i += NG * 4 * BR) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4;
+        if (r >= rows) continue;
+        float4 a = *reinterpret_cast<const float4 *>(sums + r * D + c);
+#pragma unroll
+        for (int g = 1; g < NG; ++g) {
+            const float4 b = *reinterpret_cast<const float4 *>(sums + g * gap + r * D + c);
+            a = make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+        }
+        *reinterpret_cast<float4 *>(out + (size_t)r * stride + c) = make_float4(f * a.x, f * a.y, f * a.z, f * a.w);
+    }
 }
 
-template <int D> constexpr int fwd_smem() { return (3 * BT * kStride<D> + BT * kPs) * 4; }
-template <int D> constexpr int bwd_smem() { return (4 * BT * kStride<D> + 2 * BT * kPs + 2 * BT) * 4; }
+// Groups and shared memory (floats): the block's rows, then each group's column tiles, scores and, for dk
+// and dv, the queries' lse and delta.
+template <int D> struct Fwd {
+    static constexpr int NG = D == 64 ? 4 : 2, ROWS = BQ * kStride<D>, GROUP = 2 * BC * kStride<D> + BQ * kPs;
+    static constexpr int SMEM = (ROWS + NG * GROUP) * 4;
+};
+template <int D> struct Dq {
+    static constexpr int NG = D == 64 ? 4 : 2, ROWS = 2 * BQ * kStride<D>, GROUP = 2 * BC * kStride<D> + BQ * kPs;
+    static constexpr int SMEM = (ROWS + NG * GROUP) * 4;
+};
+template <int D, int BK> struct Dkv {
+    static constexpr int NG = D == 128 ? 2 : BK == 16 ? 4 : 3, ROWS = 2 * BK * kStride<D>, GROUP = 2 * BC * kStride<D> + 2 * BK * kPs + 2 * BC;
+    static constexpr int SMEM = (ROWS + NG * GROUP) * 4;
+};
 
-template <int D> __global__ void __launch_bounds__(kThreads) attn_fwd_kernel(const AttnArgs a)
+template <int D> __global__ void __launch_bounds__(Fwd<D>::NG * 4 * BQ) attn_fwd_kernel(const AttnArgs a)
 {
-    extern __shared__ float sm[];
-    float *Q = sm, *K = Q + BT * kStride<D>, *V = K + BT * kStride<D>, *P = V + BT * kStride<D>;
+    using C = Fwd<D>;
+    extern __shared__ __align__(16) float sm[];
+    const int tid = threadIdx.x % (4 * BQ), group = threadIdx.x / (4 * BQ), tx = tid & 15, ty = tid >> 4;
+    float *Q = sm, *mine = sm + C::ROWS + group * C::GROUP, *K = mine, *V = K + BC * kStride<D>, *P = V + BC * kStride<D>;
+    __shared__ float s_m[C::NG][BQ], s_l[C::NG][BQ];
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) report_bad_seqlens(a.b, a.status);
     TileRef r;
-    if (!find_tile(a.b, gridDim.x - 1 - blockIdx.x, BT, r)) return;
-    const int h = blockIdx.y, hk = h / (a.H / a.Hkv), tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int q0 = r.tile * BT, len = r.sp.len;
-    const size_t qs = (size_t)a.H * D, ks = (size_t)a.Hkv * D;
-    const float *q = (const float *)a.q + (size_t)r.sp.bos * qs + h * D;
+    if (!find_heavy_tile(a.b, blockIdx.x, BQ, false, r)) return;
+    const int h = blockIdx.y, hk = h / (a.H / a.Hkv), q0 = r.tile * BQ, len = r.sp.len;
+    const size_t qs = (size_t)a.H * D, ks = (size_t)a.Hkv * D, qoff = (size_t)(r.sp.bos + q0) * qs + h * D;
     const float *k = (const float *)a.k + (size_t)r.sp.bos * ks + hk * D;
     const float *v = (const float *)a.v + (size_t)r.sp.bos * ks + hk * D;
-    load_tile<D>(Q, q + (size_t)q0 * qs, len - q0, qs);
+    load_tile<D, BQ>(Q, (const float *)a.q + qoff, len - q0, qs, threadIdx.x, C::NG * 4 * BQ);
+    __syncthreads();
     float o[4][D / 16] = {}, m[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
     }
-    const int last = min(q0 + BT, len) - 1;
-    for (int j = first_key_tile(q0, a.window); j * BT <= last; ++j) {
-        __syncthreads();
-        load_tile<D>(K, k + (size_t)j * BT * ks, len - j * BT, ks);
-        load_tile<D>(V, v + (size_t)j * BT * ks, len - j * BT, ks);
-        __syncthreads();
+    const int last = min(q0 + BQ, len) - 1, jb = a.window == 0 || q0 < a.window ? 0 : (q0 - a.window + 1) / BC;
+    for (int j = jb + group; j * BC <= last; j += C::NG) {
+        load_tile<D, BC>(K, k + (size_t)j * BC * ks, len - j * BC, ks, tid, 4 * BQ);
+        load_tile<D, BC>(V, v + (size_t)j * BC * ks, len - j * BC, ks, tid, 4 * BQ);
+        group_sync<4 * BQ>(group);
         float s[4][4] = {};
         dot_tile<D>(s, Q, K, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int row = q0 + ty + 16 * i;
+            const int row = q0 + 4 * ty + i;
             float top = m[i];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                s[i][n] = visible(row, j * BT + tx + 16 * n, len, a.window) ? s[i][n] * a.scale : -INFINITY;
+                s[i][n] = visible(row, j * BC + tx + 16 * n, len, a.window) ? s[i][n] * a.scale : -INFINITY;
                 top = fmaxf(top, s[i][n]);
             }
 #pragma unroll
@@ -138,7 +178,7 @@ template <int D> __global__ void __launch_bounds__(kThreads) attn_fwd_kernel(con
             for (int n = 0; n < 4; ++n) {
                 const float p = expf(s[i][n] - base);
                 sum += p;
-                P[(ty + 16 * i) * kPs + tx + 16 * n] = p;
+                P[(4 * ty + i) * kPs + tx + 16 * n] = p;
             }
 #pragma unroll
             for (int x = 8; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
@@ -147,21 +187,35 @@ template <int D> __global__ void __launch_bounds__(kThreads) attn_fwd_kernel(con
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) o[i][n] *= f;
         }
-        __syncthreads();
-        mul_tile<D, false>(o, P, V, ty, tx);
+        group_sync<4 * BQ>(group);
+        mul_tile<D>(o, P, V, ty, tx);
+        group_sync<4 * BQ>(group);
     }
+    // ---- the groups' sums joined
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (tx == 0) {
+            s_m[group][4 * ty + i] = m[i];
+            s_l[group][4 * ty + i] = l[i];
+        }
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int row = q0 + ty + 16 * i;
-        if (row >= len) continue;
-        const float inv = 1.f / l[i];
-        float *dst = (float *)a.o + ((size_t)(r.sp.bos + row) * a.H + h) * D;
+        float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int n = 0; n < D / 64; ++n)
-            *reinterpret_cast<float4 *>(dst + 64 * n + 4 * tx) =
-                make_float4(o[i][4 * n] * inv, o[i][4 * n + 1] * inv, o[i][4 * n + 2] * inv, o[i][4 * n + 3] * inv);
-        if (a.lse && tx == 0) a.lse[(size_t)(r.sp.bos + row) * a.H + h] = m[i] + logf(l[i]);
+        for (int g = 0; g < C::NG; ++g) top = fmaxf(top, s_m[g][4 * ty + i]);
+        if (top == -INFINITY) top = 0.f;  // a row past the sequence
+#pragma unroll
+        for (int g = 0; g < C::NG; ++g) sum += expf(s_m[g][4 * ty + i] - top) * s_l[g][4 * ty + i];
+        const float f = expf(m[i] - top) / sum;
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) o[i][n] *= f;
+        const int row = q0 + 4 * ty + i;
+        if (a.lse && group == 0 && tx == 0 && row < len) a.lse[(size_t)(r.sp.bos + row) * a.H + h] = top + logf(sum);
     }
+    put_sums<D>(mine, o, ty, tx);
+    __syncthreads();
+    store_sums<D, BQ, C::NG>((float *)a.o + qoff, qs, sm + C::ROWS, C::GROUP, 1.f, len - q0);
 }
 
 // delta[row, h] = sum over channels of d_o * o; 16 bytes a lane, as many lanes to a (row, head) as it
@@ -183,130 +237,138 @@ template <typename T, int D> __global__ void __launch_bounds__(256) attn_delta_k
     if (row < n && threadIdx.x % L == 0) a.delta[row] = sum;
 }
 
-// p and ds of one tile, from the scores s and the products dp = do . v, into P and S
-__device__ __forceinline__ void softmax_grad(const AttnArgs &a, float (&s)[4][4], float (&dp)[4][4], int q0, int k0,
-                                             int len, const float *lse, const float *delta, float *P, float *S, int ty,
-                                             int tx)
+template <int D> __global__ void __launch_bounds__(Dq<D>::NG * 4 * BQ) attn_dq_kernel(const AttnArgs a)
 {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int c = tx + 16 * n;
-            const float p = visible(q0 + r, k0 + c, len, a.window) ? expf(s[i][n] * a.scale - lse[r]) : 0.f;
-            P[r * kPs + c] = p;
-            S[r * kPs + c] = p == 0.f ? 0.f : p * (dp[i][n] - delta[r]);
-        }
-    }
-}
-// lse and delta of the query tile's rows
-__device__ __forceinline__ void load_stats(const AttnArgs &a, const TileRef &r, int q0, int h, float *lse, float *delta)
-{
-    if (threadIdx.x < BT) {
-        const int row = q0 + threadIdx.x;
-        const size_t at = (size_t)(r.sp.bos + row) * a.H + h;
-        lse[threadIdx.x] = row < r.sp.len ? a.lse[at] : 0.f;
-        delta[threadIdx.x] = row < r.sp.len ? a.delta[at] : 0.f;
-    }
-}
-template <int D>
-__device__ __forceinline__ void store_rows(float *dst, size_t stride, const float (&acc)[4][D / 16], float f, int rows,
-                                           int ty, int tx)
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (ty + 16 * i >= rows) continue;
-#pragma unroll
-        for (int n = 0; n < D / 64; ++n)
-            *reinterpret_cast<float4 *>(dst + (size_t)(ty + 16 * i) * stride + 64 * n + 4 * tx) =
-                make_float4(f * acc[i][4 * n], f * acc[i][4 * n + 1], f * acc[i][4 * n + 2], f * acc[i][4 * n + 3]);
-    }
-}
-
-template <int D> __global__ void __launch_bounds__(kThreads) attn_dq_kernel(const AttnArgs a)
-{
-    extern __shared__ float sm[];
-    constexpr int TS = BT * kStride<D>;
-    float *Q = sm, *O = Q + TS, *K = O + TS, *V = K + TS, *P = V + TS, *S = P + BT * kPs, *lse = S + BT * kPs, *delta = lse + BT;
+    using C = Dq<D>;
+    extern __shared__ __align__(16) float sm[];
+    const int tid = threadIdx.x % (4 * BQ), group = threadIdx.x / (4 * BQ), tx = tid & 15, ty = tid >> 4;
+    float *Q = sm, *O = sm + BQ * kStride<D>, *mine = sm + C::ROWS + group * C::GROUP, *K = mine, *V = K + BC * kStride<D>, *S = V + BC * kStride<D>;
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 32) report_bad_seqlens(a.b, a.status);
     TileRef r;
-    if (!find_tile(a.b, gridDim.x - 1 - blockIdx.x, BT, r)) return;
-    const int h = blockIdx.y, hk = h / (a.H / a.Hkv), tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int q0 = r.tile * BT, len = r.sp.len;
+    if (!find_heavy_tile(a.b, blockIdx.x, BQ, false, r)) return;
+    const int h = blockIdx.y, hk = h / (a.H / a.Hkv), q0 = r.tile * BQ, len = r.sp.len;
     const size_t qs = (size_t)a.H * D, ks = (size_t)a.Hkv * D;
     const size_t qoff = (size_t)(r.sp.bos + q0) * qs + h * D, koff = (size_t)r.sp.bos * ks + hk * D;
-    load_tile<D>(Q, (const float *)a.q + qoff, len - q0, qs);
-    load_tile<D>(O, (const float *)a.d_o + qoff, len - q0, qs);
-    load_stats(a, r, q0, h, lse, delta);
+    load_tile<D, BQ>(Q, (const float *)a.q + qoff, len - q0, qs, threadIdx.x, C::NG * 4 * BQ);
+    load_tile<D, BQ>(O, (const float *)a.d_o + qoff, len - q0, qs, threadIdx.x, C::NG * 4 * BQ);
+    float lse[4], delta[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = q0 + 4 * ty + i;
+        const size_t at = (size_t)(r.sp.bos + row) * a.H + h;
+        lse[i] = row < len ? a.lse[at] : 0.f;
+        delta[i] = row < len ? a.delta[at] : 0.f;
+    }
+    __syncthreads();
     float dq[4][D / 16] = {};
-    const int last = min(q0 + BT, len) - 1;
-    for (int j = first_key_tile(q0, a.window); j * BT <= last; ++j) {
-        __syncthreads();
-        load_tile<D>(K, (const float *)a.k + koff + (size_t)j * BT * ks, len - j * BT, ks);
-        load_tile<D>(V, (const float *)a.v + koff + (size_t)j * BT * ks, len - j * BT, ks);
-        __syncthreads();
+    const int last = min(q0 + BQ, len) - 1, jb = a.window == 0 || q0 < a.window ? 0 : (q0 - a.window + 1) / BC;
+    for (int j = jb + group; j * BC <= last; j += C::NG) {
+        load_tile<D, BC>(K, (const float *)a.k + koff + (size_t)j * BC * ks, len - j * BC, ks, tid, 4 * BQ);
+        load_tile<D, BC>(V, (const float *)a.v + koff + (size_t)j * BC * ks, len - j * BC, ks, tid, 4 * BQ);
+        group_sync<4 * BQ>(group);
         float s[4][4] = {}, dp[4][4] = {};
         dot_tile<D>(s, Q, K, ty, tx);
         dot_tile<D>(dp, O, V, ty, tx);
-        softmax_grad(a, s, dp, q0, j * BT, len, lse, delta, P, S, ty, tx);
-        __syncthreads();
-        mul_tile<D, false>(dq, S, K, ty, tx);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const bool vis = visible(q0 + 4 * ty + i, j * BC + tx + 16 * n, len, a.window);
+                S[(4 * ty + i) * kPs + tx + 16 * n] = vis ? expf(s[i][n] * a.scale - lse[i]) * (dp[i][n] - delta[i]) : 0.f;
+            }
+        group_sync<4 * BQ>(group);
+        mul_tile<D>(dq, S, K, ty, tx);
+        group_sync<4 * BQ>(group);
     }
-    store_rows<D>((float *)a.dq + qoff, qs, dq, a.scale, len - q0, ty, tx);
+    put_sums<D>(mine, dq, ty, tx);
+    __syncthreads();
+    store_sums<D, BQ, C::NG>((float *)a.dq + qoff, qs, sm + C::ROWS, C::GROUP, a.scale, len - q0);
 }
 
-template <int D> __global__ void __launch_bounds__(kThreads) attn_dkv_kernel(const AttnArgs a)
+// Rows are keys, columns queries: the groups take the (query head, query tile) pairs in turn.
+template <int D, int BK> __global__ void __launch_bounds__(Dkv<D, BK>::NG * 4 * BK) attn_dkv_kernel(const AttnArgs a)
 {
-    extern __shared__ float sm[];
-    constexpr int TS = BT * kStride<D>;
-    float *Q = sm, *O = Q + TS, *K = O + TS, *V = K + TS, *P = V + TS, *S = P + BT * kPs, *lse = S + BT * kPs, *delta = lse + BT;
+    using C = Dkv<D, BK>;
+    extern __shared__ __align__(16) float sm[];
+    const int tid = threadIdx.x % (4 * BK), group = threadIdx.x / (4 * BK), tx = tid & 15, ty = tid >> 4;
+    float *K = sm, *V = sm + BK * kStride<D>, *mine = sm + C::ROWS + group * C::GROUP, *Q = mine, *O = Q + BC * kStride<D>;
+    float *P = O + BC * kStride<D>, *S = P + BK * kPs, *lse = S + BK * kPs, *delta = lse + BC;
     TileRef r;
-    if (!find_tile(a.b, blockIdx.x, BT, r)) return;
-    const int hk = blockIdx.y, group = a.H / a.Hkv, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int k0 = r.tile * BT, len = r.sp.len;
+    if (!find_heavy_tile(a.b, blockIdx.x, BK, true, r)) return;
+    const int hk = blockIdx.y, heads = a.H / a.Hkv, k0 = r.tile * BK, len = r.sp.len;
     const size_t qs = (size_t)a.H * D, ks = (size_t)a.Hkv * D;
     const size_t koff = (size_t)(r.sp.bos + k0) * ks + hk * D;
-    load_tile<D>(K, (const float *)a.k + koff, len - k0, ks);
-    load_tile<D>(V, (const float *)a.v + koff, len - k0, ks);
+    load_tile<D, BK>(K, (const float *)a.k + koff, len - k0, ks, threadIdx.x, C::NG * 4 * BK);
+    load_tile<D, BK>(V, (const float *)a.v + koff, len - k0, ks, threadIdx.x, C::NG * 4 * BK);
+    __syncthreads();
     float dk[4][D / 16] = {}, dv[4][D / 16] = {};
     // queries k0 .. the last that still sees the tile's last key
-    const int end = a.window == 0 || a.window > len ? len : min(len, k0 + BT - 1 + a.window);
-    for (int h = hk * group; h < (hk + 1) * group; ++h)
-        for (int q0 = k0; q0 < end; q0 += BT) {
-            __syncthreads();
-            const size_t qoff = (size_t)(r.sp.bos + q0) * qs + h * D;
-            load_tile<D>(Q, (const float *)a.q + qoff, len - q0, qs);
-            load_tile<D>(O, (const float *)a.d_o + qoff, len - q0, qs);
-            load_stats(a, r, q0, h, lse, delta);
-            __syncthreads();
-            float s[4][4] = {}, dp[4][4] = {};
-            dot_tile<D>(s, Q, K, ty, tx);
-            dot_tile<D>(dp, O, V, ty, tx);
-            softmax_grad(a, s, dp, q0, k0, len, lse, delta, P, S, ty, tx);
-            __syncthreads();
-            mul_tile<D, true>(dv, P, O, ty, tx);
-            mul_tile<D, true>(dk, S, Q, ty, tx);
+    const int end = a.window == 0 || a.window > len ? len : min(len, k0 + BK - 1 + a.window), tiles = (end - k0 + BC - 1) / BC;
+    for (int i = group; i < heads * tiles; i += C::NG) {
+        const int h = hk * heads + i / tiles, q0 = k0 + i % tiles * BC;
+        const size_t qoff = (size_t)(r.sp.bos + q0) * qs + h * D;
+        load_tile<D, BC>(Q, (const float *)a.q + qoff, len - q0, qs, tid, 4 * BK);
+        load_tile<D, BC>(O, (const float *)a.d_o + qoff, len - q0, qs, tid, 4 * BK);
+        if (tid < BC) {
+            const size_t at = (size_t)(r.sp.bos + q0 + tid) * a.H + h;
+            lse[tid] = q0 + tid < len ? a.lse[at] : 0.f;
+            delta[tid] = q0 + tid < len ? a.delta[at] : 0.f;
         }
-    store_rows<D>((float *)a.dk + koff, ks, dk, a.scale, len - k0, ty, tx);
-    store_rows<D>((float *)a.dv + koff, ks, dv, 1.f, len - k0, ty, tx);
+        group_sync<4 * BK>(group);
+        float s[4][4] = {}, dp[4][4] = {};
+        dot_tile<D>(s, K, Q, ty, tx);
+        dot_tile<D>(dp, V, O, ty, tx);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const int c = tx + 16 * n, at = (4 * ty + x) * kPs + c;
+                const bool vis = visible(q0 + c, k0 + 4 * ty + x, len, a.window);
+                const float p = vis ? expf(s[x][n] * a.scale - lse[c]) : 0.f;
+                P[at] = p;
+                S[at] = vis ? p * (dp[x][n] - delta[c]) : 0.f;
+            }
+        group_sync<4 * BK>(group);
+        mul_tile<D>(dv, P, O, ty, tx);
+        mul_tile<D>(dk, S, Q, ty, tx);
+        group_sync<4 * BK>(group);
+    }
+    put_sums<D>(mine, dk, ty, tx);
+    put_sums<D>(mine + BK * D, dv, ty, tx);
+    __syncthreads();
+    store_sums<D, BK, C::NG>((float *)a.dk + koff, ks, sm + C::ROWS, C::GROUP, a.scale, len - k0);
+    store_sums<D, BK, C::NG>((float *)a.dv + koff, ks, sm + C::ROWS + BK * D, C::GROUP, 1.f, len - k0);
 }
 
-template <typename F> cudaError_t run(F kernel, int smem, dim3 grid, const AttnArgs &a, cudaStream_t s)
+template <typename F> cudaError_t run(F kernel, int smem, int threads, dim3 grid, const AttnArgs &a, cudaStream_t s)
 {
     cudaError_t e = set_smem_attr(reinterpret_cast<const void *>(kernel), smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, smem, s>>>(a);
+    kernel<<<grid, threads, smem, s>>>(a);
     return cudaGetLastError();
+}
+template <int D, int BK> cudaError_t run_dkv(const AttnArgs &a, cudaStream_t s)
+{
+    const dim3 grid((unsigned)tile_bound(a.b, BK), (unsigned)a.Hkv);
+    return run(attn_dkv_kernel<D, BK>, Dkv<D, BK>::SMEM, Dkv<D, BK>::NG * 4 * BK, grid, a, s);
+}
+template <int D> cudaError_t run_bwd(const AttnArgs &a, cudaStream_t s)
+{
+    // 16 keys to a block where 32 would not fill the SMs twice (2 x 500, 2 key heads, d 64: 48 us against
+    // 88); else 32, which read each query tile half as often (8 x 2048, 16 heads, d 128: 15.3 ms against 19.7)
+    const bool few = tile_bound(a.b, 32) * a.Hkv < 2LL * device_sms();
+    cudaError_t e = few ? run_dkv<D, 16>(a, s) : run_dkv<D, 32>(a, s);
+    const dim3 grid((unsigned)tile_bound(a.b, BQ), (unsigned)a.H);
+    return e != cudaSuccess ? e : run(attn_dq_kernel<D>, Dq<D>::SMEM, Dq<D>::NG * 4 * BQ, grid, a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_fwd_simt(const AttnArgs &a, cudaStream_t s)
 {
-    const dim3 grid((unsigned)tile_bound(a.b, BT), (unsigned)a.H);
-    return a.D == 128 ? run(attn_fwd_kernel<128>, fwd_smem<128>(), grid, a, s)
-                      : run(attn_fwd_kernel<64>, fwd_smem<64>(), grid, a, s);
+    const dim3 grid((unsigned)tile_bound(a.b, BQ), (unsigned)a.H);
+    return a.D == 128 ? run(attn_fwd_kernel<128>, Fwd<128>::SMEM, Fwd<128>::NG * 4 * BQ, grid, a, s)
+                      : run(attn_fwd_kernel<64>, Fwd<64>::SMEM, Fwd<64>::NG * 4 * BQ, grid, a, s);
 }
 
 cudaError_t launch_attn_delta(bool fp32, const AttnArgs &a, cudaStream_t s)
@@ -322,14 +384,7 @@ cudaError_t launch_attn_bwd_simt(const AttnArgs &a, cudaStream_t s)
 {
     cudaError_t e = launch_attn_delta(true, a, s);
     if (e != cudaSuccess) return e;
-    const unsigned tiles = (unsigned)tile_bound(a.b, BT);
-    const dim3 gq(tiles, (unsigned)a.H), gk(tiles, (unsigned)a.Hkv);
-    if (a.D == 128) {
-        e = run(attn_dq_kernel<128>, bwd_smem<128>(), gq, a, s);
-        return e != cudaSuccess ? e : run(attn_dkv_kernel<128>, bwd_smem<128>(), gk, a, s);
-    }
-    e = run(attn_dq_kernel<64>, bwd_smem<64>(), gq, a, s);
-    return e != cudaSuccess ? e : run(attn_dkv_kernel<64>, bwd_smem<64>(), gk, a, s);
+    return a.D == 128 ? run_bwd<128>(a, s) : run_bwd<64>(a, s);
 }
 
 }  // namespace gdn2
