@@ -14,6 +14,11 @@
 // Roles, 384 threads: warps 0-3 and 4-7 form p and ds of the tile's left and right 64 columns (a thread to
 // a row), warp 8 issues the products, warp 9 the TMA loads, warp 10 (keys' kernel) brings the rows'
 // lse and delta.  bf16 p and ds overwrite the columns of the scores that their own warps have read.
+//
+// A block stays on its SM and takes one tile after another, heavy ones first: while the warps finish a
+// tile and write its gradients, the loads and first products of the next already run.  A block to a
+// tile spent 12 of its 43 thousand cycles starting and ending (4 x 4096, window 2048).  Barriers and rings
+// go on from tile to tile; every role walks through the same tiles and counts for itself.
 #include <limits.h>
 
 #include "attn_tc.cuh"
@@ -29,7 +34,7 @@ struct BwdMaps {
 };
 struct BwdParams {
     SeqBatch b;
-    int H, Hkv, G, TQ, window;
+    int H, Hkv, G, TQ, window, qtiles, ktiles;  // tiles of queries and of keys, over all sequences
     float scale;
     const float *lse, *delta;
     __nv_bfloat16 *dq, *dk, *dv;
@@ -61,12 +66,6 @@ __device__ __forceinline__ void st64(uint32_t t, const float (&s)[64])
     for (int i = 0; i < 32; ++i) w[i] = pack_bf16x2(s[2 * i], s[2 * i + 1]);
     tmem_st32(t, w);
     tmem_wait_st();
-}
-// D (+)= A B, A = 128 x 128 bf16 left by st64 of both column halves (64 columns apart)
-__device__ __forceinline__ void mma_grad(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
-{
-    mma_tn<4>(leader, d, a, b, 0, idesc, acc);
-    mma_tn<4>(leader, d, a + 64, b, 64, idesc, 1);
 }
 // f * (this thread's row of TMEM columns [0, n)) as bf16 at dst
 template <int n> __device__ __forceinline__ void store_row(uint32_t t, float f, __nv_bfloat16 *dst, bool live)
@@ -111,21 +110,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
     extern __shared__ char raw[];
     char *sm = reinterpret_cast<char *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     char *sq = sm, *so = sq + C::TILE, *sk = so + C::TILE, *sv = sk + C::KS * C::TILE;
-    __shared__ __align__(8) uint64_t bar_q, k_full[C::KS], k_empty[C::KS], v_full[C::VS], v_empty[C::VS], s_full[2], p_full,
-        ds_ready, done, bar_drain;
+    __shared__ __align__(8) uint64_t q_full, q_empty, k_full[C::KS], k_empty[C::KS], v_full[C::VS], v_empty[C::VS], s_full[2],
+        p_full, ds_ready, done, bar_drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
     if (blockIdx.x == 0 && warp == 0) report_bad_seqlens(p.b, p.status);
-    TileRef r;
-    int hk;
-    if (!block_tile(p.b, blockIdx.x, gridDim.x / p.Hkv, p.Hkv, p.window, p.TQ, false, r, hk)) return;
-    const int len = r.sp.len, t0 = r.tile * p.TQ, nt = min(p.TQ, len - t0);
-    const int jb = p.window == 0 || t0 < p.window ? 0 : (t0 - p.window + 1) / kBN, n = (t0 + nt - 1) / kBN + 1 - jb;
-
     if (tid == 0) {
         s_abort = 0;
-        mbar_init(&bar_q, 1);
+        mbar_init(&q_full, 1);
+        mbar_init(&q_empty, 1);
         for (int i = 0; i < C::KS; ++i) {
             mbar_init(&k_full[i], 1);
             mbar_init(&k_empty[i], 1);
@@ -151,48 +145,81 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tmem = uniform(s_tmem);
 
+    // The block's work, walked through by every role: its queries' first token t0 and count nt, and its n
+    // key tiles from jb on.  `base` counts the key tiles before it, `num` the tiles of queries.
+    struct Work {
+        int hk, bos, len, t0, nt, jb, n;
+    };
+    auto find = [&](int w, Work &x) {
+        TileRef r;
+        if (!block_tile(p.b, w, p.qtiles, p.Hkv, p.window, p.TQ, false, r, x.hk)) return false;
+        x.bos = r.sp.bos;
+        x.len = r.sp.len;
+        x.t0 = r.tile * p.TQ;
+        x.nt = min(p.TQ, x.len - x.t0);
+        x.jb = p.window == 0 || x.t0 < p.window ? 0 : (x.t0 - p.window + 1) / kBN;
+        x.n = (x.t0 + x.nt - 1) / kBN + 1 - x.jb;
+        return true;
+    };
+    const int works = p.qtiles * p.Hkv;
+    int base = 0, num = 0;
+    Work x;
+    bool ok = true;
+
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int half = warp >> 2, row = tid & 127;
+        const int half = warp >> 2, row = tid & 127, tok = row / p.G;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        const int tok = row / p.G, pos = t0 + tok;
-        const bool live = row < p.TQ * p.G && tok < nt;
-        const size_t at = (size_t)(r.sp.bos + pos) * p.H + hk * p.G + (row - tok * p.G);
         const float c = p.scale * kLog2e;
-        const float lse = live ? p.lse[at] * kLog2e : 0.f, delta = live ? p.delta[at] : 0.f;
-        bool ok = true;
-        for (int it = 0; it < n; ++it) {
-            if (!(ok = wait_warp(&s_full[it & 1], (it >> 1) & 1, &s_abort, p.status))) break;
-            tc_fence_after();
-            float s[64], d[64];
-            const uint32_t ts = tmem + 128 * (it & 1) + 64 * half + lanes;
-            ld64(ts, s);
-            const int k0 = (jb + it) * kBN;
-            const bool edge = k0 + kBN - 1 > t0 || (p.window && t0 + nt - 1 - k0 >= p.window);
-            const int most = pos - k0 - 64 * half, least = p.window ? most - p.window + 1 : 0;
-            if (edge) {
+        const uint64_t c2 = pair(c, c);
+        for (int i = 0, w; ok && (w = work_at(i, works)) >= 0; ++i) {
+            if (w >= works || !find(w, x)) continue;
+            const int pos = x.t0 + tok;
+            const bool live = row < p.TQ * p.G && tok < x.nt;
+            const size_t at = (size_t)(x.bos + pos) * p.H + x.hk * p.G + (row - tok * p.G);
+            const float lse = live ? -p.lse[at] * kLog2e : 0.f, delta = live ? -p.delta[at] : 0.f;
+            const uint64_t l2 = pair(lse, lse), d2 = pair(delta, delta);
+            for (int it = 0; it < x.n; ++it) {
+                const int k = base + it;
+                if (!(ok = wait_warp(&s_full[k & 1], (k >> 1) & 1, &s_abort, p.status))) break;
+                tc_fence_after();
+                float s[64], d[64];
+                const uint32_t ts = tmem + 128 * (k & 1) + 64 * half + lanes;
+                ld64(ts, s);
+                const int k0 = (x.jb + it) * kBN;
+                const bool edge = k0 + kBN - 1 > x.t0 || (p.window && x.t0 + x.nt - 1 - k0 >= p.window);
+                const int most = pos - k0 - 64 * half, least = p.window ? most - p.window + 1 : 0;
+                if (edge) {
 #pragma unroll
-                for (int i = 0; i < 64; ++i) s[i] = i <= most && i >= least ? s[i] : -INFINITY;
+                    for (int i = 0; i < 64; ++i) s[i] = i <= most && i >= least ? s[i] : -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    unpair(fma2(pair(s[i], s[i + 1]), c2, l2), s[i], s[i + 1]);
+                    s[i] = ex2(s[i]);
+                    s[i + 1] = ex2(s[i + 1]);
+                }
+                if (!(ok = wait_warp(&p_full, k & 1, &s_abort, p.status))) break;
+                tc_fence_after();
+                ld64(tmem + kTmP + 64 * half + lanes, d);
+                if (edge) {  // values of masked keys may belong to another sequence: not 0 * (what they are)
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) d[i] = i <= most && i >= least ? d[i] : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 64; i += 2)
+                    unpair(mul2(pair(s[i], s[i + 1]), add2(pair(d[i], d[i + 1]), d2)), s[i], s[i + 1]);
+                st64(ts, s);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ds_ready);
             }
-#pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = ex2(fmaf(s[i], c, -lse));
-            if (!(ok = wait_warp(&p_full, it & 1, &s_abort, p.status))) break;
-            tc_fence_after();
-            ld64(tmem + kTmP + 64 * half + lanes, d);
-            if (edge) {  // values of masked keys may belong to another sequence: not 0 * (what they are)
-#pragma unroll
-                for (int i = 0; i < 64; ++i) d[i] = i <= most && i >= least ? d[i] : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] *= d[i] - delta;
-            st64(ts, s);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ds_ready);
-        }
-        if (ok && wait_warp(&done, 0, &s_abort, p.status)) {
+            if (!(ok = ok && wait_warp(&done, num & 1, &s_abort, p.status))) break;
             tc_fence_after();
             store_row<D / 2>(tmem + kTmQ + D / 2 * half + lanes, p.scale, p.dq + at * D + D / 2 * half, live);
+            tc_fence_before();  // the next tile's first product comes after its ds of all warps
+            base += x.n;
+            ++num;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -200,55 +227,70 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
         constexpr uint32_t kS = idesc_bf16(128, kBN, 0, 0), kG = idesc_bf16(128, D, 0, 1);
         if (warp == 8) {
             const uint32_t leader = elect();
-            bool ok = wait_warp(&bar_q, 0, &s_abort, p.status);
             auto scores = [&](int it) {
-                const int st = it % C::KS;
-                if (!wait_warp(&k_full[st], (it / C::KS) & 1, &s_abort, p.status)) return false;
+                const int k = base + it, st = k % C::KS;
+                if (!wait_warp(&k_full[st], (k / C::KS) & 1, &s_abort, p.status)) return false;
                 // keys past the sequence are another's: their ds is 0, but 0 * NaN is not
-                if ((jb + it + 1) * kBN > len) zero_rows<C::NB>(sk + st * C::TILE, len - (jb + it) * kBN);
+                if ((x.jb + it + 1) * kBN > x.len) zero_rows<C::NB>(sk + st * C::TILE, x.len - (x.jb + it) * kBN);
                 tc_fence_after();
-                mma_kk<D / 16>(leader, tmem + 128 * (it & 1), bq, bk + st * C::TILE, kS);
-                commit(leader, &s_full[it & 1]);
+                mma_kk<D / 16>(leader, tmem + 128 * (k & 1), bq, bk + st * C::TILE, kS);
+                commit(leader, &s_full[k & 1]);
                 return true;
             };
             auto products = [&](int it) {
-                const int st = it % C::VS;
-                if (!wait_warp(&v_full[st], (it / C::VS) & 1, &s_abort, p.status)) return false;
+                const int k = base + it, st = k % C::VS;
+                if (!wait_warp(&v_full[st], (k / C::VS) & 1, &s_abort, p.status)) return false;
                 tc_fence_after();
                 mma_kk<D / 16>(leader, tmem + kTmP, bo, bv + st * C::TILE, kS);
                 commit(leader, &p_full);
                 commit(leader, &v_empty[st]);
+                if (it + 1 == x.n) commit(leader, &q_empty);  // its scores came before
                 return true;
             };
-            if (ok) ok = scores(0) && products(0) && (n < 2 || scores(1));
-            for (int it = 0; ok && it < n; ++it) {
-                if (!(ok = wait_warp(&ds_ready, it & 1, &s_abort, p.status))) break;
-                tc_fence_after();
-                mma_grad(leader, tmem + kTmQ, tmem + 128 * (it & 1), bk + (it % C::KS) * C::TILE, kG, it > 0);
-                commit(leader, &k_empty[it % C::KS]);
-                if (it + 1 == n) commit(leader, &done);
-                if (it + 1 < n) ok = products(it + 1);
-                if (ok && it + 2 < n) ok = scores(it + 2);
+            for (int i = 0, w; ok && (w = work_at(i, works)) >= 0; ++i) {
+                if (w >= works || !find(w, x)) continue;
+                if (!(ok = wait_warp(&q_full, num & 1, &s_abort, p.status))) break;
+                ok = scores(0) && (x.n < 2 || scores(1)) && products(0);
+                for (int it = 0; ok && it < x.n; ++it) {
+                    const int k = base + it;
+                    if (!(ok = wait_warp(&ds_ready, k & 1, &s_abort, p.status))) break;
+                    tc_fence_after();
+                    if (it + 1 < x.n && !(ok = products(it + 1))) break;  // what the warps wait for first
+                    mma_tn<4>(leader, tmem + kTmQ, tmem + 128 * (k & 1), bk + (k % C::KS) * C::TILE, 0, kG, it > 0);
+                    mma_tn<4>(leader, tmem + kTmQ, tmem + 128 * (k & 1) + 64, bk + (k % C::KS) * C::TILE, 64, kG, 1);
+                    commit(leader, &k_empty[k % C::KS]);
+                    if (it + 1 == x.n) commit(leader, &done);
+                    if (it + 2 < x.n) ok = scores(it + 2);
+                }
+                base += x.n;
+                ++num;
             }
             if (s_abort) drain(leader, &bar_drain);
-        } else if (warp == 9 && lane == 0) {
-            mbar_expect_tx(&bar_q, 2 * C::NB * 128 * p.G * p.TQ);
-            load_tile<C::NB>(sq, &maps.q, hk * p.G, r.sp.bos + t0, &bar_q);
-            load_tile<C::NB>(so, &maps.d_o, hk * p.G, r.sp.bos + t0, &bar_q);
-            int nk = 0, nv = 0;
-            for (int it = 0; it < n; ++it) {
-                const int a = it % C::KS, b = it % C::VS, row = r.sp.bos + (jb + it) * kBN;
-                if (it >= C::KS && !wait(&k_empty[a], ((it / C::KS) & 1) ^ 1, &s_abort, p.status)) break;
-                mbar_expect_tx(&k_full[a], C::TILE);
-                load_tile<C::NB>(sk + a * C::TILE, &maps.k, hk, row, &k_full[a]);
-                ++nk;
-                if (it >= C::VS && !wait(&v_empty[b], ((it / C::VS) & 1) ^ 1, &s_abort, p.status)) break;
-                mbar_expect_tx(&v_full[b], C::TILE);
-                load_tile<C::NB>(sv + b * C::TILE, &maps.v, hk, row, &v_full[b]);
-                ++nv;
+        } else if (warp == 9) {
+            int nq = 0, nk = 0, nv = 0;  // loads issued, by lane 0
+            for (int i = 0, w; ok && (w = work_at(i, works)) >= 0; ++i) {
+                if (w >= works || !find(w, x)) continue;
+                if (lane == 0 && (nq == 0 || (ok = wait(&q_empty, (nq - 1) & 1, &s_abort, p.status)))) {
+                    mbar_expect_tx(&q_full, 2 * C::NB * 128 * p.G * p.TQ);
+                    load_tile<C::NB>(sq, &maps.q, x.hk * p.G, x.bos + x.t0, &q_full);
+                    load_tile<C::NB>(so, &maps.d_o, x.hk * p.G, x.bos + x.t0, &q_full);
+                    ++nq;
+                    for (int it = 0; it < x.n; ++it) {
+                        const int a = nk % C::KS, b = nv % C::VS, row = x.bos + (x.jb + it) * kBN;
+                        if (nk >= C::KS && !(ok = wait(&k_empty[a], ((nk / C::KS) & 1) ^ 1, &s_abort, p.status))) break;
+                        mbar_expect_tx(&k_full[a], C::TILE);
+                        load_tile<C::NB>(sk + a * C::TILE, &maps.k, x.hk, row, &k_full[a]);
+                        ++nk;
+                        if (nv >= C::VS && !(ok = wait(&v_empty[b], ((nv / C::VS) & 1) ^ 1, &s_abort, p.status))) break;
+                        mbar_expect_tx(&v_full[b], C::TILE);
+                        load_tile<C::NB>(sv + b * C::TILE, &maps.v, x.hk, row, &v_full[b]);
+                        ++nv;
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0);
             }
-            if (s_abort) {
-                mbar_wait(&bar_q, 0, 1000000000ull);
+            if (s_abort && lane == 0) {
+                if (nq) mbar_wait(&q_full, (nq - 1) & 1, 1000000000ull);
                 drain_ring(k_full, nk, C::KS);
                 drain_ring(v_full, nv, C::VS);
             }
@@ -282,23 +324,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
     char *sm = reinterpret_cast<char *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     char *sk = sm, *sv = sk + C::TILE, *sq = sv + C::TILE, *so = sq + C::ST * C::TILE;
     __shared__ __align__(16) float s_lse[2][kBM], s_delta[2][kBM];
-    __shared__ int s_pos[2][kBM];
-    __shared__ __align__(8) uint64_t bar_kv, q_full[C::ST], q_empty[C::ST], o_full[C::ST], o_empty[C::ST], stat_full[2], s_full,
-        p_full, p_ready, ds_ready, done, bar_drain;
+    __shared__ int s_tok[kBM];  // token of a packed row within its tile
+    __shared__ __align__(8) uint64_t kv_full, kv_empty, q_full[C::ST], q_empty[C::ST], o_full[C::ST], o_empty[C::ST],
+        stat_full[2], s_full, d_full, p_ready, ds_ready, done, bar_drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
-    TileRef r;
-    int hk;
-    if (!block_tile(p.b, blockIdx.x, gridDim.x / p.Hkv, p.Hkv, p.window, kBN, true, r, hk)) return;
-    const int len = r.sp.len, k0 = r.tile * kBN;
-    // query tokens that see a key of this tile: k0 .. end - 1, in tiles of TQ from the sequence's start
-    const int end = p.window == 0 || p.window > len ? len : min(len, k0 + kBN - 1 + p.window);
-    const int ib = k0 / p.TQ, n = (end + p.TQ - 1) / p.TQ - ib;
-
     if (tid == 0) {
         s_abort = 0;
-        mbar_init(&bar_kv, 1);
+        mbar_init(&kv_full, 1);
+        mbar_init(&kv_empty, 1);
         for (int i = 0; i < C::ST; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&q_empty[i], 1);
@@ -308,13 +343,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
         mbar_init(&stat_full[0], 32);
         mbar_init(&stat_full[1], 32);
         mbar_init(&s_full, 1);
-        mbar_init(&p_full, 1);
+        mbar_init(&d_full, 1);
         mbar_init(&p_ready, 8);
         mbar_init(&ds_ready, 8);
         mbar_init(&done, 1);
         mbar_init(&bar_drain, 1);
         fence_mbar_init();
     }
+    if (tid < kBM) s_tok[tid] = tid < p.TQ * p.G ? tid / p.G : INT_MAX;
     if (warp == 8) {
         tmem_alloc(&s_tmem, 512);
         tmem_relinquish();
@@ -324,49 +360,84 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
     tc_fence_after();
     const uint32_t tmem = uniform(s_tmem);
 
+    // The block's work, walked through by every role: the keys k0 .. of a sequence, and the n tiles of TQ
+    // query tokens, from tile ib of the sequence on, that see one of them.  `base` counts the query tiles
+    // before it, `num` the tiles of keys.
+    struct Work {
+        int hk, bos, len, k0, ib, n;
+    };
+    auto find = [&](int w, Work &x) {
+        TileRef r;
+        if (!block_tile(p.b, w, p.ktiles, p.Hkv, p.window, kBN, true, r, x.hk)) return false;
+        x.bos = r.sp.bos;
+        x.len = r.sp.len;
+        x.k0 = r.tile * kBN;
+        const int end = p.window == 0 || p.window > x.len ? x.len : min(x.len, x.k0 + kBN - 1 + p.window);
+        x.ib = x.k0 / p.TQ;
+        x.n = (end + p.TQ - 1) / p.TQ - x.ib;
+        return true;
+    };
+    const int works = p.ktiles * p.Hkv;
+    int base = 0, num = 0;
+    Work x;
+    bool ok = true;
+
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-        const int half = warp >> 2, row = tid & 127, key = k0 + row;
+        const int half = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t ts = tmem + 64 * half + lanes, tp = tmem + kTmP + 64 * half + lanes;
         const float c = p.scale * kLog2e;
-        bool ok = true;
-        for (int it = 0; it < n; ++it) {
-            const int st = it & 1, t0 = (ib + it) * p.TQ, nt = min(p.TQ, len - t0);
-            const bool edge = k0 + kBN - 1 > t0 || nt * p.G < kBM || (p.window && t0 + nt - 1 - k0 >= p.window);
-            if (!(ok = wait_warp(&stat_full[st], (it >> 1) & 1, &s_abort, p.status) &&
-                       wait_warp(&s_full, it & 1, &s_abort, p.status)))
-                break;
-            tc_fence_after();
-            float s[64], d[64];
-            ld64(ts, s);
-            const float *lse = s_lse[st] + 64 * half, *delta = s_delta[st] + 64 * half;
-            const int *pos = s_pos[st] + 64 * half;
+        const uint64_t c2 = pair(c, c);
+        const int *toks = s_tok + 64 * half;
+        for (int i = 0, w; ok && (w = work_at(i, works)) >= 0; ++i) {
+            if (w >= works || !find(w, x)) continue;
+            const int key = x.k0 + row;
+            for (int it = 0; it < x.n; ++it) {
+                const int k = base + it, st = k & 1, t0 = (x.ib + it) * p.TQ, nt = min(p.TQ, x.len - t0);
+                const bool edge = x.k0 + kBN - 1 > t0 || nt * p.G < kBM || (p.window && t0 + nt - 1 - x.k0 >= p.window);
+                if (!(ok = wait_warp(&stat_full[st], (k >> 1) & 1, &s_abort, p.status) &&
+                           wait_warp(&s_full, k & 1, &s_abort, p.status)))
+                    break;
+                tc_fence_after();
+                float s[64], d[64];
+                ld64(ts, s);
+                const float2 *lse = reinterpret_cast<const float2 *>(s_lse[st] + 64 * half);  // negative
+                const float2 *delta = reinterpret_cast<const float2 *>(s_delta[st] + 64 * half);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = ex2(fmaf(s[i], c, -lse[i]));
-            if (edge) {  // pos is -1 for columns that hold no row
+                for (int i = 0; i < 64; i += 2) {
+                    unpair(fma2(pair(s[i], s[i + 1]), c2, pair(lse[i / 2].x, lse[i / 2].y)), s[i], s[i + 1]);
+                    s[i] = ex2(s[i]);
+                    s[i + 1] = ex2(s[i + 1]);
+                }
+                if (edge) {  // the column's token t0 + tok sees the keys up to its own, and is one of the tile's
+                    const int least = key - t0, most = p.window ? min(nt - 1, least + p.window - 1) : nt - 1;
 #pragma unroll
-                for (int i = 0; i < 64; ++i) s[i] = key <= pos[i] && (p.window == 0 || pos[i] - key < p.window) ? s[i] : 0.f;
+                    for (int i = 0; i < 64; ++i) s[i] = toks[i] >= least && toks[i] <= most ? s[i] : 0.f;
+                }
+                st64(ts, s);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready);
+                if (!(ok = wait_warp(&d_full, k & 1, &s_abort, p.status))) break;
+                tc_fence_after();
+                ld64(tp, d);
+#pragma unroll
+                for (int i = 0; i < 64; i += 2)
+                    unpair(mul2(pair(s[i], s[i + 1]), add2(pair(d[i], d[i + 1]), pair(delta[i / 2].x, delta[i / 2].y))), s[i], s[i + 1]);
+                st64(tp, s);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ds_ready);
             }
-            st64(ts, s);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready);
-            if (!(ok = wait_warp(&p_full, it & 1, &s_abort, p.status))) break;
+            if (!(ok = ok && wait_warp(&done, num & 1, &s_abort, p.status))) break;
             tc_fence_after();
-            ld64(tp, d);
-#pragma unroll
-            for (int i = 0; i < 64; ++i) d[i] = s[i] * (d[i] - delta[i]);
-            st64(tp, d);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ds_ready);
-        }
-        if (ok && wait_warp(&done, 0, &s_abort, p.status)) {
-            tc_fence_after();
-            const size_t at = ((size_t)(r.sp.bos + key) * p.Hkv + hk) * D + D / 2 * half;
-            store_row<D / 2>(tmem + kTmV + D / 2 * half + lanes, 1.f, p.dv + at, key < len);
-            store_row<D / 2>(tmem + kTmK + D / 2 * half + lanes, p.scale, p.dk + at, key < len);
+            const size_t at = ((size_t)(x.bos + key) * p.Hkv + x.hk) * D + D / 2 * half;
+            store_row<D / 2>(tmem + kTmV + D / 2 * half + lanes, 1.f, p.dv + at, key < x.len);
+            store_row<D / 2>(tmem + kTmK + D / 2 * half + lanes, p.scale, p.dk + at, key < x.len);
+            tc_fence_before();  // the next tile's first products come after its p of all warps
+            base += x.n;
+            ++num;
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -374,12 +445,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
         constexpr uint32_t kS = idesc_bf16(128, kBM, 0, 0), kG = idesc_bf16(128, D, 0, 1);
         if (warp == 8) {
             const uint32_t leader = elect();
-            bool ok = wait_warp(&bar_kv, 0, &s_abort, p.status);
             // the tile's rows past its tokens (another sequence's, or never loaded) become zeros: their p and
             // ds are 0, but 0 * NaN is not
             auto scores = [&](int it) {
-                const int st = it % C::ST, rows = min(p.TQ, len - (ib + it) * p.TQ) * p.G;
-                if (!wait_warp(&q_full[st], (it / C::ST) & 1, &s_abort, p.status)) return false;
+                const int k = base + it, st = k % C::ST, rows = min(p.TQ, x.len - (x.ib + it) * p.TQ) * p.G;
+                if (!wait_warp(&q_full[st], (k / C::ST) & 1, &s_abort, p.status)) return false;
                 if (rows < kBM) zero_rows<C::NB>(sq + st * C::TILE, rows);
                 tc_fence_after();
                 mma_kk<D / 16>(leader, tmem, bk, bq + st * C::TILE, kS);
@@ -387,68 +457,86 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
                 return true;
             };
             auto products = [&](int it) {
-                const int st = it % C::ST, rows = min(p.TQ, len - (ib + it) * p.TQ) * p.G;
-                if (!wait_warp(&o_full[st], (it / C::ST) & 1, &s_abort, p.status)) return false;
+                const int k = base + it, st = k % C::ST, rows = min(p.TQ, x.len - (x.ib + it) * p.TQ) * p.G;
+                if (!wait_warp(&o_full[st], (k / C::ST) & 1, &s_abort, p.status)) return false;
                 if (rows < kBM) zero_rows<C::NB>(so + st * C::TILE, rows);
                 tc_fence_after();
                 mma_kk<D / 16>(leader, tmem + kTmP, bv, bo + st * C::TILE, kS);
-                commit(leader, &p_full);
+                commit(leader, &d_full);
+                if (it + 1 == x.n) commit(leader, &kv_empty);  // its scores came before
                 return true;
             };
-            if (ok) ok = scores(0) && products(0);
-            for (int it = 0; ok && it < n; ++it) {
-                const int st = it % C::ST;
-                if (!(ok = wait_warp(&p_ready, it & 1, &s_abort, p.status))) break;
-                tc_fence_after();
-                mma_grad(leader, tmem + kTmV, tmem, bo + st * C::TILE, kG, it > 0);
-                commit(leader, &o_empty[st]);
-                if (it + 1 < n && !(ok = scores(it + 1))) break;
-                if (!(ok = wait_warp(&ds_ready, it & 1, &s_abort, p.status))) break;
-                tc_fence_after();
-                mma_grad(leader, tmem + kTmK, tmem + kTmP, bq + st * C::TILE, kG, it > 0);
-                commit(leader, &q_empty[st]);
-                if (it + 1 == n) commit(leader, &done);
-                if (it + 1 < n) ok = products(it + 1);
+            for (int i = 0, w; ok && (w = work_at(i, works)) >= 0; ++i) {
+                if (w >= works || !find(w, x)) continue;
+                if (!(ok = wait_warp(&kv_full, num & 1, &s_abort, p.status))) break;
+                ok = scores(0) && products(0);
+                for (int it = 0; ok && it < x.n; ++it) {
+                    const int k = base + it, st = k % C::ST;
+                    if (!(ok = wait_warp(&p_ready, k & 1, &s_abort, p.status))) break;
+                    tc_fence_after();
+                    mma_tn<4>(leader, tmem + kTmV, tmem, bo + st * C::TILE, 0, kG, it > 0);
+                    mma_tn<4>(leader, tmem + kTmV, tmem + 64, bo + st * C::TILE, 64, kG, 1);
+                    commit(leader, &o_empty[st]);
+                    if (it + 1 < x.n && !(ok = scores(it + 1))) break;
+                    if (!(ok = wait_warp(&ds_ready, k & 1, &s_abort, p.status))) break;
+                    tc_fence_after();
+                    mma_tn<4>(leader, tmem + kTmK, tmem + kTmP, bq + st * C::TILE, 0, kG, it > 0);
+                    mma_tn<4>(leader, tmem + kTmK, tmem + kTmP + 64, bq + st * C::TILE, 64, kG, 1);
+                    commit(leader, &q_empty[st]);
+                    if (it + 1 == x.n) commit(leader, &done);
+                    if (it + 1 < x.n) ok = products(it + 1);
+                }
+                base += x.n;
+                ++num;
             }
             if (s_abort) drain(leader, &bar_drain);
-        } else if (warp == 9 && lane == 0) {
-            mbar_expect_tx(&bar_kv, 2 * C::TILE);
-            load_tile<C::NB>(sk, &maps.k, hk, r.sp.bos + k0, &bar_kv);
-            load_tile<C::NB>(sv, &maps.v, hk, r.sp.bos + k0, &bar_kv);
+        } else if (warp == 9) {
             const uint32_t bytes = C::NB * 128 * p.G * p.TQ;
-            int nq = 0, no = 0;
-            for (int it = 0; it < n; ++it) {
-                const int st = it % C::ST, row = r.sp.bos + (ib + it) * p.TQ;
-                const uint32_t par = ((it / C::ST) & 1) ^ 1;
-                if (it >= C::ST && !wait(&q_empty[st], par, &s_abort, p.status)) break;
-                mbar_expect_tx(&q_full[st], bytes);
-                load_tile<C::NB>(sq + st * C::TILE, &maps.q, hk * p.G, row, &q_full[st]);
-                ++nq;
-                if (it >= C::ST && !wait(&o_empty[st], par, &s_abort, p.status)) break;
-                mbar_expect_tx(&o_full[st], bytes);
-                load_tile<C::NB>(so + st * C::TILE, &maps.d_o, hk * p.G, row, &o_full[st]);
-                ++no;
+            int nw = 0, nq = 0, no = 0;  // loads issued, by lane 0
+            for (int i = 0, w; ok && (w = work_at(i, works)) >= 0; ++i) {
+                if (w >= works || !find(w, x)) continue;
+                if (lane == 0 && (nw == 0 || (ok = wait(&kv_empty, (nw - 1) & 1, &s_abort, p.status)))) {
+                    mbar_expect_tx(&kv_full, 2 * C::TILE);
+                    load_tile<C::NB>(sk, &maps.k, x.hk, x.bos + x.k0, &kv_full);
+                    load_tile<C::NB>(sv, &maps.v, x.hk, x.bos + x.k0, &kv_full);
+                    ++nw;
+                    for (int it = 0; it < x.n; ++it) {
+                        const int a = nq % C::ST, b = no % C::ST, row = x.bos + (x.ib + it) * p.TQ;
+                        if (nq >= C::ST && !(ok = wait(&q_empty[a], ((nq / C::ST) & 1) ^ 1, &s_abort, p.status))) break;
+                        mbar_expect_tx(&q_full[a], bytes);
+                        load_tile<C::NB>(sq + a * C::TILE, &maps.q, x.hk * p.G, row, &q_full[a]);
+                        ++nq;
+                        if (no >= C::ST && !(ok = wait(&o_empty[b], ((no / C::ST) & 1) ^ 1, &s_abort, p.status))) break;
+                        mbar_expect_tx(&o_full[b], bytes);
+                        load_tile<C::NB>(so + b * C::TILE, &maps.d_o, x.hk * p.G, row, &o_full[b]);
+                        ++no;
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0);
             }
-            if (s_abort) {
-                mbar_wait(&bar_kv, 0, 1000000000ull);
+            if (s_abort && lane == 0) {
+                if (nw) mbar_wait(&kv_full, (nw - 1) & 1, 1000000000ull);
                 drain_ring(q_full, nq, C::ST);
                 drain_ring(o_full, no, C::ST);
             }
-        } else if (warp == 10) {  // lse (log2), delta and position of the query rows
-            for (int it = 0; it < n; ++it) {
-                const int st = it & 1, t0 = (ib + it) * p.TQ, nt = min(p.TQ, len - t0);
-                // the warps have read the stage's former rows once their ds is ready
-                if (it >= 2 && !wait_warp(&ds_ready, it & 1, &s_abort, p.status)) break;
+        } else if (warp == 10) {  // -lse (log2) and -delta of the query rows
+            for (int i = 0, w; ok && (w = work_at(i, works)) >= 0; ++i) {
+                if (w >= works || !find(w, x)) continue;
+                for (int it = 0; it < x.n; ++it) {
+                    const int k = base + it, st = k & 1, t0 = (x.ib + it) * p.TQ, nt = min(p.TQ, x.len - t0);
+                    // the warps have read the stage's former rows once their ds is ready
+                    if (k >= 2 && !(ok = wait_warp(&ds_ready, k & 1, &s_abort, p.status))) break;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int row = lane + 32 * i, tok = row / p.G;
-                    const bool live = tok < nt;
-                    const size_t at = (size_t)(r.sp.bos + t0 + tok) * p.H + hk * p.G + (row - tok * p.G);
-                    s_lse[st][row] = live ? p.lse[at] * kLog2e : 0.f;
-                    s_delta[st][row] = live ? p.delta[at] : 0.f;
-                    s_pos[st][row] = live ? t0 + tok : -1;
+                    for (int i = 0; i < 4; ++i) {
+                        const int row = lane + 32 * i, tok = row / p.G;
+                        const bool live = row < p.TQ * p.G && tok < nt;
+                        const size_t at = (size_t)(x.bos + t0 + tok) * p.H + x.hk * p.G + (row - tok * p.G);
+                        s_lse[st][row] = live ? -p.lse[at] * kLog2e : 0.f;
+                        s_delta[st][row] = live ? -p.delta[at] : 0.f;
+                    }
+                    mbar_arrive(&stat_full[st]);
                 }
-                mbar_arrive(&stat_full[st]);
+                base += x.n;
             }
         }
     }
@@ -494,9 +582,11 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs &a, cudaStream_t s)
         return cudaErrorInvalidValue;
     cudaError_t e = launch_attn_delta(false, a, s);
     if (e != cudaSuccess) return e;
-    const long long nq = tile_bound(a.b, p.TQ) * a.Hkv, nk = tile_bound(a.b, kBN) * a.Hkv;
-    if (nq > INT_MAX || nk > INT_MAX) return cudaErrorInvalidValue;
-    const dim3 gq((unsigned)nq), gk((unsigned)nk);
+    const long long nq = tile_bound(a.b, p.TQ) * a.Hkv, nk = tile_bound(a.b, kBN) * a.Hkv, sms = device_sms();
+    if (nq > INT_MAX / 2 || nk > INT_MAX / 2) return cudaErrorInvalidValue;
+    p.qtiles = (int)(nq / a.Hkv);
+    p.ktiles = (int)(nk / a.Hkv);
+    const dim3 gq((unsigned)(nq < sms ? nq : sms)), gk((unsigned)(nk < sms ? nk : sms));
     if (a.D == 128) {
         e = run(attn_dkv_tc_kernel<128>, DkvCfg<128>::SMEM, gk, maps, p, s);
         return e != cudaSuccess ? e : run(attn_dq_tc_kernel<128>, DqCfg<128>::SMEM, gq, maps, p, s);

@@ -101,36 +101,53 @@ __device__ __forceinline__ void drain(uint32_t leader, uint64_t *bar)
     __syncwarp();
 }
 
-// D (128 x N, fp32, TMEM) (+)= A (128 x 16 ks) B^T: both operands K-major SW128 tiles in column blocks of
-// 64 channels, kBoxBytes apart.
-template <int kSteps>
+// D (128 x N, fp32, TMEM) = A (128 x 16 ks) B^T: both operands K-major SW128 tiles in column blocks of 64
+// channels, A of 128 rows, B of kRows.
+template <int kSteps, int kRows = 128>
 __device__ __forceinline__ void mma_kk(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc)
 {
     const uint64_t da = tc::sdesc_sw128(a, 16, 1024), db = tc::sdesc_sw128(b, 16, 1024);
 #pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks) {
-        const uint64_t off = (ks >> 2) * (kBoxBytes >> 4) + (ks & 3) * 2;  // in the descriptors' units of 16 bytes
-        mma_ss(leader, d, da + off, db + off, idesc, ks > 0);
+    for (int ks = 0; ks < kSteps; ++ks) {  // offsets in the descriptors' units of 16 bytes
+        const uint64_t in = (ks & 3) * 2;
+        mma_ss(leader, d, da + (ks >> 2) * (kBoxBytes >> 4) + in, db + (ks >> 2) * (kRows * 8) + in, idesc, ks > 0);
     }
 }
+// The same with A (bf16, 8 columns a step) in TMEM.
+template <int kSteps, int kRows>
+__device__ __forceinline__ void mma_tk(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc)
+{
+    const uint64_t db = tc::sdesc_sw128(b, 16, 1024);
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks)
+        mma_ts(leader, d, a + 8 * ks, db + (ks >> 2) * (kRows * 8) + (ks & 3) * 2, idesc, ks > 0);
+}
 // D (128 x N) (+)= A B with A (128 x 16 ks, bf16, 8 columns a step) in TMEM and B the same number of rows, from
-// `row` on, of a tile [128 rows][N channels] in shared memory, N-major.
-template <int kSteps>
+// `row` on, of a tile [kRows rows][N channels] in shared memory, N-major.
+template <int kSteps, int kRows = 128>
 __device__ __forceinline__ void mma_tn(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, int row, uint32_t idesc, uint32_t acc)
 {
-    const uint64_t db = tc::sdesc_sw128(b + row * 128, kBoxBytes, 1024);
+    const uint64_t db = tc::sdesc_sw128(b + row * 128, kRows * 128, 1024);
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks) mma_ts(leader, d, a + 8 * ks, db + ks * 128, idesc, ks > 0 ? 1u : acc);
 }
+// The same with A (128 x 128) a K-major tile in shared memory.
+__device__ __forceinline__ void mma_kn(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
+{
+    const uint64_t da = tc::sdesc_sw128(a, 16, 1024), db = tc::sdesc_sw128(b, kBoxBytes, 1024);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+        mma_ss(leader, d, da + (ks >> 2) * (kBoxBytes >> 4) + (ks & 3) * 2, db + ks * 128, idesc, ks > 0 ? 1u : acc);
+}
 
-// Zeros in rows [from, 128) of an SW128 tile of kBlocks column blocks, by one warp, visible to the
+// Zeros in rows [from, kRows) of an SW128 tile of kBlocks column blocks, by one warp, visible to the
 // tensor core's reads that the warp issues afterwards.
-template <int kBlocks> __device__ __forceinline__ void zero_rows(char *tile, int from)
+template <int kBlocks, int kRows = 128> __device__ __forceinline__ void zero_rows(char *tile, int from)
 {
     const int lane = threadIdx.x & 31;
-    for (int i = from * 8 + lane; i < 128 * 8; i += 32)
+    for (int i = from * 8 + lane; i < kRows * 8; i += 32)
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) *reinterpret_cast<uint4 *>(tile + b * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
+        for (int b = 0; b < kBlocks; ++b) *reinterpret_cast<uint4 *>(tile + b * (kRows * 128) + i * 16) = make_uint4(0, 0, 0, 0);
     tc::fence_proxy_async_smem();
     __syncwarp();
 }
@@ -175,6 +192,15 @@ __device__ __forceinline__ bool block_tile(const SeqBatch &b, int block, int til
     r.tile = uniform(r.tile);
     r.sp.len = uniform(r.sp.len);
     return ok;
+}
+
+// The block's k'th piece of work where pieces lie in order of falling cost: back and forth, so that no
+// block gets the heaviest of every round (dk/dv at d = 64, packed: 127 us forth only).  Past the
+// last piece's round -1; a number of `works` or more is no work, but others may follow.
+__device__ __forceinline__ int work_at(int k, int works)
+{
+    const int g = gridDim.x;
+    return (long long)k * g >= works ? -1 : k * g + (k & 1 ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
 }
 
 // TMA view of a bf16 [rows][heads][D] tensor: boxes of (64 channels, box_heads, box_rows).
