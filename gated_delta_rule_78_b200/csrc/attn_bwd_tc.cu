@@ -42,6 +42,10 @@ struct BwdParams {
 };
 
 constexpr int kThreads = 384;
+// Of 16 pairs of weights, those formed on the FMA pipe: the special-function unit's 16 values a clock are
+// half of a tile's time, and the warps have nothing else to do meanwhile (dk/dv 375 -> 361 us, dq 271 ->
+// 268 us at 4 x 4096; with 7 of 16 360 and 274; the forward's softmax, which waits for its products, gains nothing).
+constexpr int kFma = 5;
 
 // one tile by TMA: its column blocks at dst
 template <int NB>
@@ -57,6 +61,17 @@ __device__ __forceinline__ void ld64(uint32_t t, float (&s)[64])
     tmem_ld32(t, reinterpret_cast<uint32_t(&)[32]>(s[0]));
     tmem_ld32(t + 32, reinterpret_cast<uint32_t(&)[32]>(s[32]));
     tmem_wait_ld();
+}
+// 2^x of a pair, number i of a row's 32, in place; every one by ex2 where exact zeros (2^-inf) are wanted
+__device__ __forceinline__ void weights(uint64_t x, int i, bool exact, float &a, float &b)
+{
+    if (!exact && i % 16 * kFma / 16 != (i % 16 + 1) * kFma / 16) {  // spread evenly
+        ex2_fma(x, a, b);
+    } else {
+        unpair(x, a, b);
+        a = ex2(a);
+        b = ex2(b);
+    }
 }
 // this thread's row of 64 values as bf16 into 32 columns
 __device__ __forceinline__ void st64(uint32_t t, const float (&s)[64])
@@ -86,12 +101,6 @@ template <int n> __device__ __forceinline__ void store_row(uint32_t t, float f, 
         }
     }
 }
-// after a wait that gave up: the loads of a ring, `n` of them issued, end before the block's memory is free
-__device__ __forceinline__ void drain_ring(uint64_t *full, int n, int stages)
-{
-    for (int i = n > stages ? n - stages : 0; i < n; ++i) mbar_wait(&full[i % stages], (i / stages) & 1, 1000000000ull);
-}
-
 // ------------------------------------------------------------------ dq
 // TMEM: S of even and odd key tiles, dP = dO V^T, dQ.  The tensor core forms S two tiles ahead and dP one
 // ahead of the warps; K waits in shared memory from S to dQ, three stages of it.
@@ -193,11 +202,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
 #pragma unroll
                     for (int i = 0; i < 64; ++i) s[i] = i <= most && i >= least ? s[i] : -INFINITY;
                 }
+                if (edge) {
 #pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    unpair(fma2(pair(s[i], s[i + 1]), c2, l2), s[i], s[i + 1]);
-                    s[i] = ex2(s[i]);
-                    s[i + 1] = ex2(s[i + 1]);
+                    for (int i = 0; i < 64; i += 2) weights(fma2(pair(s[i], s[i + 1]), c2, l2), i / 2, true, s[i], s[i + 1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 64; i += 2) weights(fma2(pair(s[i], s[i + 1]), c2, l2), i / 2, false, s[i], s[i + 1]);
                 }
                 if (!(ok = wait_warp(&p_full, k & 1, &s_abort, p.status))) break;
                 tc_fence_after();
@@ -405,11 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
                 const float2 *lse = reinterpret_cast<const float2 *>(s_lse[st] + 64 * half);  // negative
                 const float2 *delta = reinterpret_cast<const float2 *>(s_delta[st] + 64 * half);
 #pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    unpair(fma2(pair(s[i], s[i + 1]), c2, pair(lse[i / 2].x, lse[i / 2].y)), s[i], s[i + 1]);
-                    s[i] = ex2(s[i]);
-                    s[i + 1] = ex2(s[i + 1]);
-                }
+                for (int i = 0; i < 64; i += 2)
+                    weights(fma2(pair(s[i], s[i + 1]), c2, pair(lse[i / 2].x, lse[i / 2].y)), i / 2, false, s[i], s[i + 1]);
                 if (edge) {  // the column's token t0 + tok sees the keys up to its own, and is one of the tile's
                     const int least = key - t0, most = p.window ? min(nt - 1, least + p.window - 1) : nt - 1;
 #pragma unroll

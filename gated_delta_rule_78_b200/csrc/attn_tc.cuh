@@ -101,6 +101,12 @@ __device__ __forceinline__ void drain(uint32_t leader, uint64_t *bar)
     __syncwarp();
 }
 
+// after a wait that gave up: the loads of a ring, `n` of them issued, end before the block's memory is free
+__device__ __forceinline__ void drain_ring(uint64_t *full, int n, int stages)
+{
+    for (int i = n > stages ? n - stages : 0; i < n; ++i) tc::mbar_wait(&full[i % stages], (i / stages) & 1, 1000000000ull);
+}
+
 // D (128 x N, fp32, TMEM) = A (128 x 16 ks) B^T: both operands K-major SW128 tiles in column blocks of 64
 // channels, A of 128 rows, B of kRows.
 template <int kSteps, int kRows = 128>
@@ -158,6 +164,28 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+// 2^x of two values on the FMA pipe, for x in [-126, 127] (below: as -126).  x = n + f, n its nearest
+// integer, found by adding 1.5 * 2^23; 2^f = sum (f ln 2)^i / i! on [-1/2, 1/2] by its Chebyshev
+// interpolant of degree 5 (2.6e-7 relative in fp32); n is added to the exponent.
+__device__ __forceinline__ void ex2_fma(uint64_t x, float &a, float &b)
+{
+    float x0, x1;
+    unpair(x, x0, x1);
+    x = pair(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+    const uint64_t magic = pair(12582912.f, 12582912.f), minus = pair(-12582912.f, -12582912.f);
+    const uint64_t t = add2(x, magic), n = add2(t, minus);
+    const uint64_t f = fma2(n, pair(-1.f, -1.f), x);
+    constexpr float k[6] = {1.f, 0.693147182f, 0.240221068f, 0.0555035695f, 0.00967603177f, 0.00133908633f};
+    uint64_t y = pair(k[5], k[5]);
+#pragma unroll
+    for (int i = 4; i >= 0; --i) y = fma2(y, f, pair(k[i], k[i]));
+    float y0, y1, t0, t1;
+    unpair(y, y0, y1);
+    unpair(t, t0, t1);
+    a = __int_as_float(__float_as_int(y0) + (__float_as_int(t0) << 23));
+    b = __int_as_float(__float_as_int(y1) + (__float_as_int(t1) << 23));
+}
+
 // Four e4m3 values as two pairs of bf16 (exact: e4m3 -> f16 -> f32 -> bf16).
 __device__ __forceinline__ void e4m3x4_bf16(uint32_t x, uint32_t &lo, uint32_t &hi)
 {
