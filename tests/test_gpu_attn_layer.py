@@ -1,0 +1,222 @@
+"""The attention layer's operators together, as training and serving use them, next to the recurrence."""
+import pytest
+import torch
+
+import attn_ref as R
+
+pytestmark = pytest.mark.gpu
+H, HKV, D, ROT = 8, 2, 64, 32
+INV = torch.tensor([10000.0 ** (-2 * i / ROT) for i in range(ROT // 2)])
+
+
+def weights(seed):
+    g = torch.Generator().manual_seed(seed)
+    return 1 + 0.1 * torch.randn(D, generator=g), 1 + 0.1 * torch.randn(D, generator=g)
+
+
+def tokens(n, seed, dt=torch.bfloat16):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn(n, h, D, generator=g).to(dt) for h in (H, HKV, HKV, H)]
+
+
+def positions(lens):
+    return torch.cat([torch.arange(n, dtype=torch.int32) for n in lens])
+
+
+@pytest.mark.parametrize("window", [0, 50])
+def test_training_step_fp32(cuda_lib, window):
+    """Norm, rotation and attention forward, and the gradients back to q, k, v and the norm's weights,
+    against autograd in 64 bits.  fp32 throughout: the bound is the framework's 1e-4 of the largest."""
+    g = cuda_lib
+    lens = [70, 1, 129]
+    q, k, v, do = tokens(sum(lens), 1, torch.float32)
+    wq, wk = weights(2)
+    pos = positions(lens)
+    c = lambda *x: [t.cuda() for t in x]  # noqa: E731
+    dq_, dk_, dv_, ddo, dwq_, dwk_, dpos, dinv = c(q, k, v, do, wq, wk, pos, INV)
+    cu = R.lens_to_cu(lens).cuda()
+    qr, kr = g.gdn2_qk_rope(dq_, dk_, dwq_, dwk_, dpos, dinv)
+    o, lse = g.gdn2_attn_fwd_varlen(qr, kr, dv_, cu, window=window)
+    ga = g.gdn2_attn_bwd_varlen(qr, kr, dv_, o, lse, ddo, cu, window=window)
+    gr = g.gdn2_qk_rope_bwd(dq_, dk_, dwq_, dwk_, dpos, dinv, ga["dq"], ga["dk"])
+    assert g.gdn2_sync_status() == 0
+
+    leaves = [t.double().requires_grad_() for t in (q, k, v, wq, wk)]
+    a, b, vv, aw, bw = leaves
+    qq, kk = R.rope(a, aw, pos, INV, False, 1e-6, 1.0, True), R.rope(b, bw, pos, INV, False, 1e-6, 1.0, True)
+    outs, at = [], 0
+    for n in lens:
+        s = torch.einsum("qhd,khd->hqk", qq[at:at + n], kk[at:at + n].repeat_interleave(H // HKV, 1)) * D ** -0.5
+        s = s.masked_fill(~R.mask_of(0, n, n, window), -float("inf"))
+        outs.append(torch.einsum("hqk,khd->qhd", torch.softmax(s, -1), vv[at:at + n].repeat_interleave(H // HKV, 1)))
+        at += n
+    ref = torch.cat(outs)
+    grads = torch.autograd.grad(ref, leaves, do.double())
+    got = (gr["dq"], gr["dk"], ga["dv"], gr["dq_weight"], gr["dk_weight"])
+    for name, x, y in zip(("o", "dq", "dk", "dv", "dwq", "dwk"), (o, *got), (ref.detach(), *grads)):
+        err = float((x.cpu().double() - y).abs().max() / y.abs().max())
+        assert err <= 1e-4, (name, err)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_serving_equals_the_prompt(cuda_lib, e4m3):
+    """A prompt written to the cache in chunks and then token by token, each step's attention against the
+    64-bit attention over what the cache holds; with a bf16 cache that is the whole-prompt attention."""
+    g = cuda_lib
+    lens, page = [150, 37], 16
+    steps = [[64, 20], [70, 1], [1, 1], [1, 0], [14, 15]]  # new tokens of each sequence, summing to lens
+    q, k, v, _ = tokens(sum(lens), 3)
+    wq, wk = weights(4)
+    pos = positions(lens)
+    qr, kr = (t.cpu() for t in g.gdn2_qk_rope(q.cuda(), k.cuda(), wq.cuda(), wk.cuda(), pos.cuda(), INV.cuda()))
+    width = -(-max(lens) // page)
+    dt = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    kc, vc = (torch.zeros(2 * width, page, HKV, D, dtype=dt, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(2 * width, page, HKV, device="cuda") if e4m3 else None for _ in range(2))
+    table = torch.randperm(2 * width, generator=torch.Generator().manual_seed(1)).to(torch.int32).view(2, width).cuda()
+    held = lambda x: (lambda y, s: y * s.double()[..., None])(*R.quantise(x)) if e4m3 else x.double()  # noqa: E731
+    off, done, o_all, lse_all = [0, lens[0]], [0, 0], torch.empty_like(q), torch.empty(sum(lens), H)
+    for step in steps:
+        rows = torch.cat([torch.arange(off[i] + done[i], off[i] + done[i] + n) for i, n in enumerate(step)])
+        done = [a + b for a, b in zip(done, step)]
+        cu, kv = R.lens_to_cu(step).cuda(), torch.tensor(done, dtype=torch.int32).cuda()
+        g.gdn2_cache_write(kr[rows].cuda(), v[rows].cuda(), kc, vc, cu, kv, table, ks, vs)
+        o, lse = g.gdn2_attn_cached(qr[rows].cuda(), kc, vc, cu, kv, table, ks, vs)
+        assert g.gdn2_sync_status() == 0
+        o_all[rows], lse_all[rows] = o.cpu(), lse.cpu()
+    assert done == lens
+    for i, n in enumerate(lens):
+        r = slice(off[i], off[i] + n)
+        kk, vv = held(kr[r]), held(v[r])
+        for h in range(H):
+            x = R.head(qr[r, h], kk[:, h // (H // HKV)], vv[:, h // (H // HKV)], 0, 0, D ** -0.5, torch.bfloat16)
+            R.check(o_all[r, h], x["o"], x["o_tol"], "o")
+            R.check(lse_all[r, h], x["lse"], x["lse_tol"], "lse")
+    # the cache read back gives what was written
+    kb, vb = g.gdn2_cache_read(kc, vc, R.lens_to_cu(lens).cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), table, ks, vs,
+                               total_T=sum(lens))
+    assert torch.equal(kb.cpu(), held(kr).float().bfloat16()) and torch.equal(vb.cpu(), held(v).float().bfloat16())
+    # a chunk of the read-back rows through the whole-sequence call
+    o, _ = g.gdn2_attn_fwd_varlen(qr.cuda(), kb, vb, R.lens_to_cu(lens).cuda())
+    ref = R.attention(qr, kb.cpu(), vb.cpu(), [(0, lens[0]), (lens[0], lens[1])], 0, D ** -0.5)
+    R.check(o, ref["o"], ref["o_tol"], "o over the read-back cache")
+
+
+def test_next_to_the_recurrence(cuda_lib):
+    """A recurrent layer's output as the values of an attention layer, in one captured graph, replayed on
+    new inputs: the same as the calls made one by one."""
+    from synthetic_inputs import make_inputs
+    g = cuda_lib
+    B, T = 1, 200
+
+    def inputs(seed):
+        x = make_inputs(B, T, HKV, D, D, dtype="bf16", seed=seed)
+        q, k, _, _ = tokens(T, seed)
+        return {**{n: x[n] for n in ("q", "k", "v", "log_alpha", "b", "w")}, "aq": q[None], "ak": k[None]}
+
+    pos, inv = torch.arange(T, dtype=torch.int32).view(1, T).cuda(), INV.cuda()
+    wq, wk = (t.cuda() for t in weights(5))
+
+    def layer(x):
+        y, _ = g.gdn2_chunk_fwd(x["q"], x["k"], x["v"], x["log_alpha"], x["b"], x["w"])
+        a, b = g.gdn2_qk_rope(x["aq"], x["ak"], wq, wk, pos, inv)
+        o, lse = g.gdn2_attn_fwd(a, b, y, window=64)
+        gr = g.gdn2_attn_bwd(a, b, y, o, lse, o, window=64)
+        return o, gr["dv"], *g.gdn2_qk_rope_bwd(x["aq"], x["ak"], wq, wk, pos, inv, gr["dq"], gr["dk"]).values()
+
+    x = {n: t.cuda() for n, t in inputs(1).items()}
+    eager = layer(x)  # an eager step's tensors live on while the graph is captured
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer(x)
+    new = inputs(2)
+    for n in x:
+        x[n].copy_(new[n])
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    want = layer({n: t.cuda() for n, t in new.items()})
+    assert g.gdn2_sync_status() == 0
+    for a, b, e in zip(out, want, eager):
+        assert torch.equal(a, b) and not torch.equal(a, e)
+
+
+def test_calls_on_two_streams_at_once(cuda_lib):
+    """Independent calls of every operator on two streams together: the same as one after the other."""
+    g = cuda_lib
+    lens = [300, 41]
+    cu = R.lens_to_cu(lens).cuda()
+    pos, inv = positions(lens).cuda(), INV.cuda()
+    kv = torch.tensor(lens, dtype=torch.int32).cuda()
+    table = torch.arange(2 * 19, dtype=torch.int32).view(2, 19).cuda()
+
+    def run(x, stream):
+        q, k, v, do = x
+        a, b = g.gdn2_qk_rope(q, k, None, None, pos, inv, stream=stream)
+        o, lse = g.gdn2_attn_fwd_varlen(a, b, v, cu, stream=stream)
+        gr = g.gdn2_attn_bwd_varlen(a, b, v, o, lse, do, cu, stream=stream)
+        rb = g.gdn2_qk_rope_bwd(q, k, None, None, pos, inv, gr["dq"], gr["dk"], stream=stream)
+        with torch.cuda.stream(stream):
+            kc, vc = (torch.zeros(38, 16, HKV, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        g.gdn2_cache_write(b, v, kc, vc, cu, kv, table, stream=stream)
+        oc, _ = g.gdn2_attn_cached(a, kc, vc, cu, kv, table, stream=stream)
+        return [o, lse, gr["dv"], *rb.values(), oc, kc]
+
+    xs = [[t.cuda() for t in tokens(sum(lens), s)] for s in (10, 11)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    together = [run(x, s) for x, s in zip(xs, streams) for _ in range(1)]
+    torch.cuda.synchronize()
+    for x, got in zip(xs, together):
+        for a, b in zip(run(x, streams[0]), got):
+            streams[0].synchronize()
+            assert torch.equal(a, b)
+    assert g.gdn2_sync_status() == 0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_cache_past_32_bit_offsets(cuda_lib, rows, e4m3):
+    """Pages whose elements and bytes lie past 2^32: written, read back, attended to."""
+    g = cuda_lib
+    hkv, d, page, pages = 8, 128, 64, 66000 if e4m3 else 34000  # 4.3e9 and 2.2e9 elements a tensor
+    dt = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    kc, vc = (torch.empty(pages, page, hkv, d, dtype=dt, device="cuda") for _ in range(2))
+    ks, vs = (torch.empty(pages, page, hkv, device="cuda") if e4m3 else None for _ in range(2))
+    n = 200
+    table = torch.tensor([[pages - 1, 0, pages - 2, pages - 3]], dtype=torch.int32).cuda()
+    gen = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(n, hkv, d, generator=gen).bfloat16() for _ in range(2))
+    q = torch.randn(rows, hkv, d, generator=gen).bfloat16()
+    kv, cu = torch.tensor([n], dtype=torch.int32).cuda(), R.lens_to_cu([n]).cuda()
+    g.gdn2_cache_write(k.cuda(), v.cuda(), kc, vc, cu, kv, table, ks, vs)
+    kb, vb = (t.cpu() for t in g.gdn2_cache_read(kc, vc, cu, kv, table, ks, vs, total_T=n))
+    o, lse = g.gdn2_attn_cached(q.cuda(), kc, vc, R.lens_to_cu([rows]).cuda(), kv, table, ks, vs)
+    assert g.gdn2_sync_status() == 0
+    held = [(lambda y, s: y * s.double()[..., None])(*R.quantise(x)) if e4m3 else x.double() for x in (k, v)]
+    for got, x in zip((kb, vb), held):
+        assert torch.equal(got, x.float().bfloat16())
+    for h in range(hkv):
+        x = R.head(q[:, h], held[0][:, h], held[1][:, h], n - rows, 0, d ** -0.5, torch.bfloat16)
+        R.check(o[:, h], x["o"], x["o_tol"], "o")
+        R.check(lse[:, h], x["lse"], x["lse_tol"], "lse")
+
+
+def test_stale_rows_behind_a_sequence_do_not_matter(cuda_lib):
+    """What lies behind a sequence in its last page (here NaN) changes nothing, bit for bit, for one token
+    and for a chunk, by box and by copy."""
+    g = cuda_lib
+    for page in (64, 7):
+        for rows in (1, 60):
+            n = 75
+            gen = torch.Generator().manual_seed(rows)
+            k, v, q = (torch.randn(m, HKV, D, generator=gen).bfloat16().cuda() for m in (n, n, rows))
+            pages = -(-n // page)
+            table = torch.arange(pages, dtype=torch.int32).view(1, -1).cuda()
+            outs = []
+            for fill in (0.0, float("nan"), float("inf")):
+                kc, vc = (torch.full((pages, page, HKV, D), fill, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+                kv = torch.tensor([n], dtype=torch.int32).cuda()
+                g.gdn2_cache_write(k, v, kc, vc, R.lens_to_cu([n]).cuda(), kv, table)
+                outs.append(g.gdn2_attn_cached(q, kc, vc, R.lens_to_cu([rows]).cuda(), kv, table)[0])
+            assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2]), (page, rows)
