@@ -108,52 +108,34 @@ __device__ __forceinline__ void drain_ring(uint64_t *full, int n, int stages)
 }
 
 // D (128 x N, fp32, TMEM) = A (128 x 16 ks) B^T: both operands K-major SW128 tiles in column blocks of 64
-// channels, A of 128 rows, B of kRows.
-template <int kSteps, int kRows = 128>
+// channels, of 128 rows.
+template <int kSteps>
 __device__ __forceinline__ void mma_kk(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc)
 {
     const uint64_t da = tc::sdesc_sw128(a, 16, 1024), db = tc::sdesc_sw128(b, 16, 1024);
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks) {  // offsets in the descriptors' units of 16 bytes
         const uint64_t in = (ks & 3) * 2;
-        mma_ss(leader, d, da + (ks >> 2) * (kBoxBytes >> 4) + in, db + (ks >> 2) * (kRows * 8) + in, idesc, ks > 0);
+        mma_ss(leader, d, da + (ks >> 2) * (kBoxBytes >> 4) + in, db + (ks >> 2) * (kBoxBytes >> 4) + in, idesc, ks > 0);
     }
 }
-// The same with A (bf16, 8 columns a step) in TMEM.
-template <int kSteps, int kRows>
-__device__ __forceinline__ void mma_tk(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc)
-{
-    const uint64_t db = tc::sdesc_sw128(b, 16, 1024);
-#pragma unroll
-    for (int ks = 0; ks < kSteps; ++ks)
-        mma_ts(leader, d, a + 8 * ks, db + (ks >> 2) * (kRows * 8) + (ks & 3) * 2, idesc, ks > 0);
-}
 // D (128 x N) (+)= A B with A (128 x 16 ks, bf16, 8 columns a step) in TMEM and B the same number of rows, from
-// `row` on, of a tile [kRows rows][N channels] in shared memory, N-major.
-template <int kSteps, int kRows = 128>
+// `row` on, of a tile [128 rows][N channels] in shared memory, N-major.
+template <int kSteps>
 __device__ __forceinline__ void mma_tn(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, int row, uint32_t idesc, uint32_t acc)
 {
-    const uint64_t db = tc::sdesc_sw128(b + row * 128, kRows * 128, 1024);
+    const uint64_t db = tc::sdesc_sw128(b + row * 128, kBoxBytes, 1024);
 #pragma unroll
     for (int ks = 0; ks < kSteps; ++ks) mma_ts(leader, d, a + 8 * ks, db + ks * 128, idesc, ks > 0 ? 1u : acc);
 }
-// The same with A (128 x 128) a K-major tile in shared memory.
-__device__ __forceinline__ void mma_kn(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
-{
-    const uint64_t da = tc::sdesc_sw128(a, 16, 1024), db = tc::sdesc_sw128(b, kBoxBytes, 1024);
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
-        mma_ss(leader, d, da + (ks >> 2) * (kBoxBytes >> 4) + (ks & 3) * 2, db + ks * 128, idesc, ks > 0 ? 1u : acc);
-}
-
-// Zeros in rows [from, kRows) of an SW128 tile of kBlocks column blocks, by one warp, visible to the
+// Zeros in rows [from, 128) of an SW128 tile of kBlocks column blocks, by one warp, visible to the
 // tensor core's reads that the warp issues afterwards.
-template <int kBlocks, int kRows = 128> __device__ __forceinline__ void zero_rows(char *tile, int from)
+template <int kBlocks> __device__ __forceinline__ void zero_rows(char *tile, int from)
 {
     const int lane = threadIdx.x & 31;
-    for (int i = from * 8 + lane; i < kRows * 8; i += 32)
+    for (int i = from * 8 + lane; i < kBN * 8; i += 32)
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) *reinterpret_cast<uint4 *>(tile + b * (kRows * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+        for (int b = 0; b < kBlocks; ++b) *reinterpret_cast<uint4 *>(tile + b * kBoxBytes + i * 16) = make_uint4(0, 0, 0, 0);
     tc::fence_proxy_async_smem();
     __syncwarp();
 }
@@ -234,12 +216,18 @@ __device__ __forceinline__ int work_at(int k, int works)
 // TMA view of a bf16 [rows][heads][D] tensor: boxes of (64 channels, box_heads, box_rows).
 bool make_head_map(CUtensorMap *m, const void *ptr, long long rows, int heads, int D, int box_heads, int box_rows);
 
-// 32 bytes in one store
+// 32 bytes in one store, in two where p is aligned to 16 bytes only (as a caller's tensor may be)
 __device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8])
 {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
+    if (((uintptr_t)p & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        uint4 *d = static_cast<uint4 *>(p);
+        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
 }  // namespace attn

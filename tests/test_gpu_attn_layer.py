@@ -220,3 +220,73 @@ def test_stale_rows_behind_a_sequence_do_not_matter(cuda_lib):
                 g.gdn2_cache_write(k, v, kc, vc, R.lens_to_cu([n]).cuda(), kv, table)
                 outs.append(g.gdn2_attn_cached(q, kc, vc, R.lens_to_cu([rows]).cuda(), kv, table)[0])
             assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2]), (page, rows)
+
+
+def at_16(t):
+    """t's values at an address that 16 divides and 32 does not, which is all that the entry points ask for."""
+    n = t.numel() * t.element_size()
+    raw = torch.empty(n + 64, dtype=torch.uint8, device="cuda")
+    at = (16 - raw.data_ptr()) % 32
+    x = raw[at:at + n].view(t.dtype).view(t.shape)
+    assert x.data_ptr() % 32 == 16
+    return x.copy_(t)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tensors_aligned_to_16_bytes_only(cuda_lib, D, dt):
+    """Rotation and attention, forward and backward, with every tensor and workspace at an odd multiple of
+    16 bytes: bit for bit what they give elsewhere."""
+    g = cuda_lib
+    lens, gen = [150, 37], torch.Generator().manual_seed(7)
+    q, k, v, do = (torch.randn(sum(lens), h, D, generator=gen).to(dt).cuda() for h in (H, HKV, HKV, H))
+    w, inv, pos, cu = torch.ones(D).cuda(), INV.cuda(), positions(lens).cuda(), R.lens_to_cu(lens).cuda()
+
+    def calls(f, e):
+        a, b, c, d, ww, pp, ii, cc = (f(t) for t in (q, k, v, do, w, pos, inv, cu))
+        qr, kr = g.gdn2_qk_rope(a, b, ww, ww, pp, ii, q_out=e(a), k_out=e(b))
+        lse = e(torch.empty(sum(lens), H, device="cuda"))
+        o, _ = g.gdn2_attn_fwd_varlen(qr, kr, c, cc, o=e(a), lse=lse)
+        ws = e(torch.empty(g.gdn2_attn_workspace_size(dt, len(lens), max(lens), H, HKV, D), dtype=torch.uint8, device="cuda"))
+        ga = g.gdn2_attn_bwd_varlen(qr, kr, c, o, lse, d, cc, out={"dq": e(a), "dk": e(b), "dv": e(c)}, workspace=ws)
+        gr = g.gdn2_qk_rope_bwd(a, b, ww, ww, pp, ii, ga["dq"], ga["dk"])
+        assert g.gdn2_sync_status() == 0
+        return [qr, kr, o, lse, *(ga[n] for n in ("dq", "dk", "dv")), *(gr[n] for n in ("dq", "dk", "dq_weight", "dk_weight"))]
+
+    for x, y in zip(calls(lambda t: t, torch.empty_like), calls(at_16, lambda t: at_16(torch.zeros_like(t)))):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens,page", [([1, 2], 16), ([150, 37], 16), ([150, 37], 12)])
+def test_cache_aligned_to_16_bytes_only(cuda_lib, lens, page, D, e4m3):
+    """... and the cache's calls: few and many rows, with and without a split key axis."""
+    g = cuda_lib
+    gen = torch.Generator().manual_seed(8)
+    kv = [n + 600 for n in lens]
+    q, k, v = (torch.randn(n, h, D, generator=gen).bfloat16().cuda() for n, h in ((sum(lens), H), (sum(kv), HKV), (sum(kv), HKV)))
+    width = -(-max(kv) // page)
+    table = torch.arange(2 * width, dtype=torch.int32).view(2, width).cuda()
+    dt = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    cus, kvs = [R.lens_to_cu(n).cuda() for n in (lens, kv)], torch.tensor(kv, dtype=torch.int32).cuda()
+
+    def calls(f, e):
+        kc, vc = (f(torch.zeros(2 * width * page * HKV * D, dtype=torch.uint8, device="cuda").view(torch.uint8)
+                    if e4m3 else torch.zeros(2 * width * page * HKV * D, dtype=torch.bfloat16, device="cuda"))
+                  .view(dt).view(2 * width, page, HKV, D) for _ in range(2))
+        ks, vs = (f(torch.zeros(2 * width, page, HKV, device="cuda")) if e4m3 else None for _ in range(2))
+        a, b, c, t, n, c0, c1 = (f(x) for x in (q, k, v, table, kvs, *cus))
+        g.gdn2_cache_write(b, c, kc, vc, c1, n, t, ks, vs)
+        kb, vb = g.gdn2_cache_read(kc, vc, c1, n, t, ks, vs, k=e(b), v=e(c))
+        out = [kb, vb]
+        for window in (0, 40):
+            ws = e(torch.empty(max(16, g.gdn2_attn_cached_workspace_size(2, sum(lens), H, HKV, D, window, width, page)),
+                               dtype=torch.uint8, device="cuda"))
+            out += g.gdn2_attn_cached(a, kc, vc, c0, n, t, ks, vs, window=window, o=e(a),
+                                      lse=e(torch.empty(sum(lens), H, device="cuda")), workspace=ws)
+        assert g.gdn2_sync_status() == 0
+        return out
+
+    for x, y in zip(calls(lambda t: t, torch.empty_like), calls(at_16, lambda t: at_16(torch.zeros_like(t)))):
+        assert torch.equal(x, y)
