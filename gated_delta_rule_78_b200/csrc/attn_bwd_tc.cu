@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
     __shared__ __align__(16) float s_lse[2][kBM], s_delta[2][kBM];
     __shared__ int s_tok[kBM];  // token of a packed row within its tile
     __shared__ __align__(8) uint64_t kv_full, kv_empty, q_full[C::ST], q_empty[C::ST], o_full[C::ST], o_empty[C::ST],
-        stat_full[2], s_full, d_full, p_ready, ds_ready, done, bar_drain;
+        stat_full[2], stat_empty[2], s_full, d_full, p_ready, ds_ready, done, bar_drain;
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -352,6 +352,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
         }
         mbar_init(&stat_full[0], 32);
         mbar_init(&stat_full[1], 32);
+        mbar_init(&stat_empty[0], 8);
+        mbar_init(&stat_empty[1], 8);
         mbar_init(&s_full, 1);
         mbar_init(&d_full, 1);
         mbar_init(&p_ready, 8);
@@ -435,7 +437,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
                 st64(tp, s);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ds_ready);
+                if (lane == 0) {
+                    mbar_arrive(&stat_empty[st]);
+                    mbar_arrive(&ds_ready);
+                }
             }
             if (!(ok = ok && wait_warp(&done, num & 1, &s_abort, p.status))) break;
             tc_fence_after();
@@ -531,8 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dkv_tc_kernel(const __grid_c
                 if (w >= works || !find(w, x)) continue;
                 for (int it = 0; it < x.n; ++it) {
                     const int k = base + it, st = k & 1, t0 = (x.ib + it) * p.TQ, nt = min(p.TQ, x.len - t0);
-                    // the warps have read the stage's former rows once their ds is ready
-                    if (k >= 2 && !(ok = wait_warp(&ds_ready, k & 1, &s_abort, p.status))) break;
+                    // a barrier to a stage: ds_ready's own may be two tiles further when this warp, which may have
+                    // searched a long batch for its next tile, comes to look
+                    if (k >= 2 && !(ok = wait_warp(&stat_empty[st], ((k >> 1) & 1) ^ 1, &s_abort, p.status))) break;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int row = lane + 32 * i, tok = row / p.G;

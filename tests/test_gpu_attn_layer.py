@@ -290,3 +290,28 @@ def test_cache_aligned_to_16_bytes_only(cuda_lib, lens, page, D, e4m3):
 
     for x, y in zip(calls(lambda t: t, torch.empty_like), calls(at_16, lambda t: at_16(torch.zeros_like(t)))):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 70])
+def test_many_short_sequences(cuda_lib, window, D):
+    """A long packed batch, several tiles of keys and of queries to a block, each found by a search that
+    takes longer than the tile before it."""
+    g = cuda_lib
+    gen = torch.Generator().manual_seed(11)
+    lens = torch.randint(0, 40, (1500,), generator=gen).tolist()
+    lens[700], lens[1400] = 300, 200
+    n = sum(lens)
+    q, k, v, do = (torch.randn(n, h, D, generator=gen).bfloat16() for h in (4, 2, 2, 4))
+    cu = R.lens_to_cu(lens).cuda()
+    qd, kd, vd, dod = (t.cuda() for t in (q, k, v, do))
+    o, lse = g.gdn2_attn_fwd_varlen(qd, kd, vd, cu, window=window)
+    got = {"o": o, "lse": lse, **g.gdn2_attn_bwd_varlen(qd, kd, vd, o, lse, dod, cu, window=window)}
+    assert g.gdn2_sync_status() == 0
+    spans, at = [], 0
+    for m in lens:
+        spans.append((at, m))
+        at += m
+    ref = R.attention(q, k, v, spans, window, D ** -0.5, do)
+    for name in ("o", "lse", "dq", "dk", "dv"):
+        R.check(got[name], ref[name], ref[name + "_tol"], name)
