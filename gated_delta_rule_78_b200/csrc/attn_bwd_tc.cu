@@ -11,6 +11,14 @@
 // accumulated in memory would need 5 products a pair instead of 7, and fp32 atomics.  p and ds are
 // rounded to bf16 for their products (2^-9 of each term), everything else is fp32.
 //
+// o comes rounded to bf16, and what that does to delta is a fixed share of p in every ds of a row, which
+// does not average out; most in a sequence's first rows, whose few weights are large.  Where all keys of
+// a tile of queries are one tile, the dq kernel takes delta from the weights themselves, sum_j p_ij (do_i .
+// v_j), and leaves it for the keys' kernel, which runs after it.  Relative errors of dq and dk of random
+// sequences of 1 to 3 tokens: 2.8e-3 and 3.1e-3 -> 2.3e-3 and 2.5e-3, of 1500: 2.5e-3 -> 2.4e-3 (their own
+// rounding alone: 1.7e-3).  (Corrected in every row by its sum of ds, which should be 0: dk is no better,
+// and dq takes 303 instead of 266 us at 4 x 4096, window 2048.)
+//
 // Roles, 384 threads: warps 0-3 and 4-7 form p and ds of the tile's left and right 64 columns (a thread to
 // a row), warp 8 issues the products, warp 9 the TMA loads, warp 10 (keys' kernel) brings the rows'
 // lse and delta.  bf16 p and ds overwrite the columns of the scores that their own warps have read.
@@ -36,7 +44,8 @@ struct BwdParams {
     SeqBatch b;
     int H, Hkv, G, TQ, window, qtiles, ktiles;  // tiles of queries and of keys, over all sequences
     float scale;
-    const float *lse, *delta;
+    const float *lse;
+    float *delta;  // [rows, H]: do . o, in a sequence's first rows then the dq kernel's
     __nv_bfloat16 *dq, *dk, *dv;
     int *status;
 };
@@ -120,7 +129,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
     char *sm = reinterpret_cast<char *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     char *sq = sm, *so = sq + C::TILE, *sk = so + C::TILE, *sv = sk + C::KS * C::TILE;
     __shared__ __align__(8) uint64_t q_full, q_empty, k_full[C::KS], k_empty[C::KS], v_full[C::VS], v_empty[C::VS], s_full[2],
-        p_full, ds_ready, done, bar_drain;
+        p_full, ds_ready, sum_full, done, bar_drain;
+    __shared__ float s_sum[2][kBM];  // by half of the columns, and row
     __shared__ uint32_t s_tmem;
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
@@ -141,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
         mbar_init(&s_full[1], 1);
         mbar_init(&p_full, 1);
         mbar_init(&ds_ready, 8);
+        mbar_init(&sum_full, 8);
         mbar_init(&done, 1);
         mbar_init(&bar_drain, 1);
         fence_mbar_init();
@@ -181,13 +192,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const float c = p.scale * kLog2e;
         const uint64_t c2 = pair(c, c);
+        uint32_t ones = 0;  // tiles of queries with one tile of keys, so far
         for (int i = 0, w; ok && (w = work_at(i, works)) >= 0; ++i) {
             if (w >= works || !find(w, x)) continue;
             const int pos = x.t0 + tok;
             const bool live = row < p.TQ * p.G && tok < x.nt;
             const size_t at = (size_t)(x.bos + pos) * p.H + x.hk * p.G + (row - tok * p.G);
             const float lse = live ? -p.lse[at] * kLog2e : 0.f, delta = live ? -p.delta[at] : 0.f;
-            const uint64_t l2 = pair(lse, lse), d2 = pair(delta, delta);
+            const uint64_t l2 = pair(lse, lse);
+            uint64_t d2 = pair(delta, delta);
             for (int it = 0; it < x.n; ++it) {
                 const int k = base + it;
                 if (!(ok = wait_warp(&s_full[k & 1], (k >> 1) & 1, &s_abort, p.status))) break;
@@ -215,6 +228,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dq_tc_kernel(const __grid_co
                 if (edge) {  // values of masked keys may belong to another sequence: not 0 * (what they are)
 #pragma unroll
                     for (int i = 0; i < 64; ++i) d[i] = i <= most && i >= least ? d[i] : 0.f;
+                }
+                if (x.n == 1) {  // delta from the row's weights: the halves' sums, by way of shared memory
+                    uint64_t a2 = 0, b2 = 0;
+#pragma unroll
+                    for (int i = 0; i < 64; i += 4) {
+                        a2 = fma2(pair(s[i], s[i + 1]), pair(d[i], d[i + 1]), a2);
+                        b2 = fma2(pair(s[i + 2], s[i + 3]), pair(d[i + 2], d[i + 3]), b2);
+                    }
+                    float a, b;
+                    unpair(add2(a2, b2), a, b);
+                    s_sum[half][row] = a + b;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sum_full);
+                    if (!(ok = wait_warp(&sum_full, ones & 1, &s_abort, p.status))) break;
+                    // (written again after the next tile's s_full, which follows all warps' ds)
+                    const float sum = a + b + s_sum[half ^ 1][row];
+                    d2 = pair(-sum, -sum);
+                    if (live && half == 0) p.delta[at] = sum;
+                    ++ones;
                 }
 #pragma unroll
                 for (int i = 0; i < 64; i += 2)
@@ -600,12 +632,13 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs &a, cudaStream_t s)
     p.qtiles = (int)(nq / a.Hkv);
     p.ktiles = (int)(nk / a.Hkv);
     const dim3 gq((unsigned)(nq < sms ? nq : sms)), gk((unsigned)(nk < sms ? nk : sms));
+    // dq first: its delta of the sequences' first rows is the better one
     if (a.D == 128) {
-        e = run(attn_dkv_tc_kernel<128>, DkvCfg<128>::SMEM, gk, maps, p, s);
-        return e != cudaSuccess ? e : run(attn_dq_tc_kernel<128>, DqCfg<128>::SMEM, gq, maps, p, s);
+        e = run(attn_dq_tc_kernel<128>, DqCfg<128>::SMEM, gq, maps, p, s);
+        return e != cudaSuccess ? e : run(attn_dkv_tc_kernel<128>, DkvCfg<128>::SMEM, gk, maps, p, s);
     }
-    e = run(attn_dkv_tc_kernel<64>, DkvCfg<64>::SMEM, gk, maps, p, s);
-    return e != cudaSuccess ? e : run(attn_dq_tc_kernel<64>, DqCfg<64>::SMEM, gq, maps, p, s);
+    e = run(attn_dq_tc_kernel<64>, DqCfg<64>::SMEM, gq, maps, p, s);
+    return e != cudaSuccess ? e : run(attn_dkv_tc_kernel<64>, DkvCfg<64>::SMEM, gk, maps, p, s);
 }
 
 }  // namespace gdn2

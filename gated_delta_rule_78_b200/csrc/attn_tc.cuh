@@ -146,14 +146,21 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
-// 2^x of two values on the FMA pipe, for x in [-126, 127] (below: as -126).  x = n + f, n its nearest
+// the larger of two values, NaN where one is
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+// 2^x of two values on the FMA pipe, for x in [-126, 127] (below: as -126; NaN: infinite in bf16).  x = n + f, n its nearest
 // integer, found by adding 1.5 * 2^23; 2^f = sum (f ln 2)^i / i! on [-1/2, 1/2] by its Chebyshev
 // interpolant of degree 5 (2.6e-7 relative in fp32); n is added to the exponent.
 __device__ __forceinline__ void ex2_fma(uint64_t x, float &a, float &b)
 {
     float x0, x1;
     unpair(x, x0, x1);
-    x = pair(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+    x = pair(max_nan(x0, -126.f), max_nan(x1, -126.f));
     const uint64_t magic = pair(12582912.f, 12582912.f), minus = pair(-12582912.f, -12582912.f);
     const uint64_t t = add2(x, magic), n = add2(t, minus);
     const uint64_t f = fma2(n, pair(-1.f, -1.f), x);

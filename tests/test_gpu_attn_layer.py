@@ -315,3 +315,19 @@ def test_many_short_sequences(cuda_lib, window, D):
     ref = R.attention(q, k, v, spans, window, D ** -0.5, do)
     for name in ("o", "lse", "dq", "dk", "dv"):
         R.check(got[name], ref[name], ref[name + "_tol"], name)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_nan_is_not_lost(cuda_lib, D):
+    """A NaN in one query: every gradient that it has a part in says so, in every channel."""
+    g = cuda_lib
+    q, k, v, do = (torch.randn(1, 300, 2, D, generator=torch.Generator().manual_seed(i)).bfloat16().cuda() for i in range(4))
+    q[0, 200, 1, 5] = float("nan")
+    o, lse = g.gdn2_attn_fwd(q, k, v)
+    r = g.gdn2_attn_bwd(q, k, v, o, lse, do)
+    assert g.gdn2_sync_status() == 0
+    bad = {n: ~torch.isfinite(t[0]) for n, t in {"o": o, "lse": lse[..., None], **r}.items()}
+    for n in ("o", "lse", "dq"):  # the row alone
+        assert bad[n][200, 1].all() and bad[n].sum() == bad[n][200, 1].numel(), n
+    for n in ("dk", "dv"):  # the keys that the row sees (other keys of its sequence and head may have it: 0 * NaN)
+        assert bad[n][:201, 1].all() and not bad[n][:, 0].any(), n
