@@ -252,7 +252,7 @@ struct CachedPlan {
     bool tc;
     int splits;
 };
-CachedPlan cached_plan(int n, long long rows, int H, int Hkv, int window, long long capacity);
+CachedPlan cached_plan(bool e4m3, int n, long long rows, int H, int Hkv, int window, long long capacity);
 size_t cached_workspace_bytes(long long rows, int H, int D, int splits);
 cudaError_t launch_attn_cached(const CachedArgs &a, bool tc, cudaStream_t s);
 cudaError_t launch_attn_cached_tc(const CachedArgs &a, cudaStream_t s);

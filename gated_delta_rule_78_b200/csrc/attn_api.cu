@@ -273,8 +273,13 @@ size_t gdn2_attn_cached_workspace_size(gdn2_dtype dt, int N, int total_T, int H,
         check_cache(GDN2_CACHE_BF16, dt, N, total_T, Hkv, D, max_pages, 1, page_size) != GDN2_OK)
         return 0;
     window = effective_window(window, (long long)max_pages * page_size);
-    const CachedPlan plan = cached_plan(N, total_T, H, Hkv, window, (long long)max_pages * page_size);
-    return cached_workspace_bytes(total_T, H, D, plan.splits);
+    size_t most = 0;  // for either type of cache
+    for (bool e4m3 : {false, true}) {
+        const CachedPlan plan = cached_plan(e4m3, N, total_T, H, Hkv, window, (long long)max_pages * page_size);
+        const size_t need = cached_workspace_bytes(total_T, H, D, plan.splits);
+        most = need > most ? need : most;
+    }
+    return most;
 }
 
 gdn2_status gdn2_attn_cached(gdn2_cache_type type, gdn2_dtype dt, int N, int total_T, int H, int Hkv, int D,
@@ -290,7 +295,7 @@ gdn2_status gdn2_attn_cached(gdn2_cache_type type, gdn2_dtype dt, int N, int tot
     if (st == GDN2_OK && type == GDN2_CACHE_E4M3) st = check_ptrs({k_scale, v_scale});
     if (st != GDN2_OK) return st;
     window = effective_window(window, (long long)max_pages * page_size);
-    const CachedPlan plan = cached_plan(N, total_T, H, Hkv, window, (long long)max_pages * page_size);
+    const CachedPlan plan = cached_plan(type == GDN2_CACHE_E4M3, N, total_T, H, Hkv, window, (long long)max_pages * page_size);
     const size_t need = cached_workspace_bytes(total_T, H, D, plan.splits);
     if (need) {
         if (!workspace || ws_bytes < need) return GDN2_ERR_WORKSPACE;

@@ -33,6 +33,7 @@ using tc::pack_bf16x2;
 using tc::smem_u32;
 
 constexpr int kWarps = 4;
+constexpr int kManyRows = 1024;  // rows of outputs that fill the SMs at a warp to a row
 constexpr float kGrow = 8.f;    // growth of the maximum (log2) that moves the reference
 constexpr float kWeight = 6.f;  // e4m3: log2 of the weight at the reference
 
@@ -609,21 +610,30 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 }  // namespace
 
-CachedPlan cached_plan(int n, long long rows, int H, int Hkv, int window, long long capacity)
+// Measured with H = 16, Hkv = 4, D = 128, times in us with the join.
+CachedPlan cached_plan(bool e4m3, int n, long long rows, int H, int Hkv, int window, long long capacity)
 {
     const int G = H / Hkv;
     CachedPlan plan;
-    // rows a sequence and key head, on average: up to 32 the step is bound by the cache's bytes
-    plan.tc = rows * G > 32LL * n;
+    // Rows a sequence and key head, on average: few leave the step bound by the cache's bytes, and the
+    // tensor core's tile of 128 rows empty; the rows kernel reads the keys once to every 16.  Rows kernel against
+    // tiles, 8 sequences over 8192 keys: 16 rows 40 and 59, 20 rows 52 and 42, 32 rows 58 and 43; 64 over 2048:
+    // 32 rows 104 and 71 (but 2 over 2048: 16 and 18).  e4m3, whose bytes are half and whose tiles wait for their
+    // conversion, 8 over 8192: 32 rows 49 and 102, 64 rows 80 and 103, 128 rows 144 and 104.
+    plan.tc = rows * G > (e4m3 ? 64LL : 16LL) * n;
     const long long keys = window > 0 && window + rows < capacity ? window + rows : capacity;
     if (plan.tc) {
-        const long long blocks = (rows * G / 256 + n) * Hkv;
-        const long long want = ceil_div(device_sms(), blocks);
+        // As many parts as blocks run at once, if sequences are alike.  512 tokens over 32768 keys: 4 parts 132,
+        // 5 (a second wave) 193, 8 142; 128 tokens: 16 parts 51, 13 59, 8 72; 4 x 512 over 16384, 128 blocks
+        // of their own: 1 part 227, 2 252.
+        const long long blocks = n * ((rows * G + 256LL * n - 1) / (256LL * n)) * Hkv, want = device_sms() / blocks;
         plan.splits = (int)(want < keys / 512 ? want : keys / 512);
     } else {
+        // Two waves of blocks (one sequence over 32768 keys: 1 wave 24, 2 24, 4 28), and ragged lengths: no block
+        // reads more than 2048 keys (64 sequences of 64 to 8192 keys, e4m3: 39; 1024 40; any number 55)
         const long long blocks = (long long)n * Hkv;
         long long want = ceil_div(2LL * device_sms(), blocks);
-        const long long even = ceil_div(keys, 2048);  // ragged lengths: no block reads more than 2048 keys
+        const long long even = ceil_div(keys, 2048);
         if (want < even) want = even;
         plan.splits = (int)(want < keys / 256 ? want : keys / 256);
     }
@@ -658,7 +668,9 @@ cudaError_t launch_attn_cached(const CachedArgs &a, bool use_tc, cudaStream_t s)
     if (use_tc) {
         e = launch_attn_cached_tc(a, s);
     } else {
-        const bool wide = a.b.rows * p.G > 8LL * a.b.n;  // more than 8 rows a sequence, on average
+        // more than 8 rows a sequence, on average (64 sequences over 4096 keys: 12 rows 111 us, by eights 139; 4 rows
+        // 108, by eights 105)
+        const bool wide = a.b.rows * p.G > 8LL * a.b.n;
         const int rows = wide ? 16 : 8;
         long long keys = (long long)a.c.width * a.c.page;
         if (a.window > 0 && a.window + rows < keys) keys = a.window + rows;
@@ -670,7 +682,9 @@ cudaError_t launch_attn_cached(const CachedArgs &a, bool use_tc, cudaStream_t s)
     }
     if (e != cudaSuccess || a.splits == 1) return e;
     const long long rows = a.b.rows * a.H;
-    if (a.splits > 8) (a.D == 128 ? attn_join_kernel<128, 8> : attn_join_kernel<64, 8>)<<<(unsigned)rows, 256, 0, s>>>(p);
+    // 8 warps to a row where parts are many and rows too few to fill the SMs (16 rows, 37 parts: 24 us in all,
+    // a warp to a row 38; 2048 rows, 16 parts: 52 and 50; 32768 rows: 454 and 379)
+    if (a.splits > 8 && rows <= kManyRows) (a.D == 128 ? attn_join_kernel<128, 8> : attn_join_kernel<64, 8>)<<<(unsigned)rows, 256, 0, s>>>(p);
     else (a.D == 128 ? attn_join_kernel<128, 1> : attn_join_kernel<64, 1>)<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
     return cudaGetLastError();
 }

@@ -130,7 +130,8 @@ cudaError_t launch_cache_copy(bool read, const SeqBatch &b, int Hkv, int D, cons
                               int *status, cudaStream_t s)
 {
     const int R = 32 / (D / 8);
-    // a warp moves one pass of rows while that leaves few enough warps, more of them for long batches
+    // a warp moves one pass of rows while that leaves few enough warps, four of them for long batches (8 heads, D =
+    // 128, bf16, one pass against four: 256 tokens 3.9 us and 5.5, 2048 7.3 and 7.8, 8192 19 and 15.5, 32768 66 and 47)
     const int passes = (2 * Hkv + R - 1) / R;
     const int chunks = b.rows * passes <= (1 << 15) ? passes : (passes + 3) / 4;
     CopyArgs a{b, Hkv, chunks, c, k, v, status};
