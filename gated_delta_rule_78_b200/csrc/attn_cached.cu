@@ -21,6 +21,9 @@
 //
 // Cut into parts, each part writes its normalised output and log-sum; a second kernel joins them,
 // in a fixed order.
+//
+// 256 sequences of 256 to 8192 keys, 16 heads on 4, D = 128, e4m3: 129 us and 5 for the joining (4.7 TB/s; sequences
+// alike, 2048 keys each: 98 us).  One sequence over 32768 keys, bf16: 18.5 and 5 us, launch and latency.
 #include "attn_tc.cuh"
 
 namespace gdn2 {

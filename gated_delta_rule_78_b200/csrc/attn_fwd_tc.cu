@@ -15,6 +15,11 @@
 // tile's warps form its weights.  TMEM: S_A, S_B (128 columns each), O_A, O_B (D columns each).
 // With D = 128 that is all of it: P overwrites its own S, and the next S waits for P V.  With D = 64 P
 // has 64 columns of its own, and the next S is formed as soon as the warps hold this one in registers.
+//
+// 4 x 4096, 16 heads, D = 128, window 2048: 219 us, 206 GFLOP, 940 TFLOP/s.  A step (a key tile for A and B) takes 1.9 us
+// of which the products are 1.5: with D = 128 S of the next tile cannot start before this P V, and the two
+// tiles' softmax fills only most of that gap.  With D = 64 it takes 1.7 us, bound by the warps: 16 exponentials a
+// clock are 70% of it.
 #include <limits.h>
 
 #include "attn_tc.cuh"

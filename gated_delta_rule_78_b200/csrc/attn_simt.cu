@@ -12,6 +12,9 @@
 // 16-byte loads of both operands from shared memory: 12 wavefronts of them to 64 FMAs of a warp, so
 // bound by the FP32 pipe first and shared memory next.  The backward runs two kernels, so that no sum
 // depends on the order in which blocks run.
+//
+// 2 x 500 tokens, 4 heads on 2, D = 64: forward 28 us, delta 2, dk and dv 48, dq 31.  At such sizes a block's
+// few tiles one after another are the time, and in a tile the loads, for which nothing else is ready.
 #include "attn.cuh"
 
 namespace gdn2 {

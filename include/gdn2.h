@@ -324,7 +324,8 @@ GDN2_API gdn2_status gdn2_prologue(int flags, gdn2_dtype dt, int N, int H, int D
  * cache with the attention that reads it for serving.  The conventions at the top of this file
  * hold, with these additions:
  *  - q and o have H heads, k and v Hkv heads; for attention Hkv divides H, H / Hkv <= 64, and query
- *    head h reads key head h / (H / Hkv).  One head size D in {64, 128}.  Rows x heads < 2^31.
+ *    head h reads key head h / (H / Hkv).  One head size D in {64, 128}.  Rows <= 2^30, rows x heads
+ *    < 2^31 (GDN2_ERR_UNSUPPORTED beyond).
  *  - Packed batches: cu_seqlens, DEVICE int32 [N + 1], 0 = c_0 <= c_1 <= ... <= c_N <= total_T.
  *    Empty sequences are allowed; rows behind c_N belong to no sequence and the outputs' rows there
  *    are left as they were (a padded batch).  A sequence whose entries are invalid is skipped, its
@@ -400,7 +401,7 @@ GDN2_API size_t gdn2_attn_workspace_size(gdn2_dtype dt, int N, int T, int H, int
  *   kv_lens:     DEVICE int32 [N], the sequence's length WITH its new tokens: the rows that
  *                cu_seqlens gives sequence n are its positions kv_lens[n] - (c_{n+1} - c_n) ..
  *                kv_lens[n] - 1.
- * dt is GDN2_BF16 (GDN2_F32 gives GDN2_ERR_UNSUPPORTED).  A page size is any number >= 1;
+ * Scales are >= 0.  dt is GDN2_BF16 (GDN2_F32 gives GDN2_ERR_UNSUPPORTED).  A page size is any number >= 1;
  * max_pages * page_size <= 2^30, num_pages * page_size < 2^31.  A kv_lens entry below the sequence's
  * new tokens or above max_pages * page_size skips the sequence, a page outside the cache skips the
  * row (attention reads zeros for it), and either records GDN2_ERR_PAGES.
@@ -427,7 +428,7 @@ GDN2_API gdn2_status gdn2_cache_read(gdn2_cache_type type, gdn2_dtype dt, int N,
  * Attention of each sequence's newest tokens (one for a decode step, a chunk of a long prompt) over
  * the paged cache, which already holds them.  q, o: [total_T, H, D]; lse: fp32 [total_T, H] or NULL.
  * The query at position i sees the cached positions j <= i (and j > i - window), as gdn2_attn_fwd.
- *   workspace: gdn2_attn_cached_workspace_size() bytes; 0 needs none (NULL allowed).  The calls that
+ *   workspace: gdn2_attn_cached_workspace_size() bytes (for either type of cache); 0 needs none (NULL allowed).  The calls that
  *   share one must be ordered, captured graphs among them.
  */
 GDN2_API gdn2_status gdn2_attn_cached(gdn2_cache_type type, gdn2_dtype dt, int N, int total_T, int H, int Hkv, int D,

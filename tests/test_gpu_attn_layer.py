@@ -331,3 +331,56 @@ def test_nan_is_not_lost(cuda_lib, D):
         assert bad[n][200, 1].all() and bad[n].sum() == bad[n][200, 1].numel(), n
     for n in ("dk", "dv"):  # the keys that the row sees (other keys of its sequence and head may have it: 0 * NaN)
         assert bad[n][:201, 1].all() and not bad[n][:, 0].any(), n
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("news", [[1, 1, 0], [3, 1, 2], [70, 20, 0]])
+def test_padded_batches_and_shared_pages(cuda_lib, news, e4m3):
+    """Serving with a batch padded to a fixed number of rows and sequences that share their first pages: the
+    cache and the outputs behind the last row stay as they were, and the sharing changes nothing."""
+    g = cuda_lib
+    page, shared, gen = 16, 5, torch.Generator().manual_seed(12)
+    kv = [90 + 3 * n for n in news]
+    kv = [max(a, n + shared * page) for a, n in zip(kv, news)]
+    n, tail, width = sum(news), 9, 24
+    q, k, v = (torch.randn(n + tail, h, D, generator=gen).bfloat16() for h in (H, HKV, HKV))
+    for t in (q, k, v):
+        t[n:] = float("nan")
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    dt = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    pages = 3 * width
+    raw = [torch.randint(0, 120, (pages, page, HKV, D), generator=gen).to(torch.uint8).view(dt) if e4m3 else
+           torch.randn(pages, page, HKV, D, generator=gen).bfloat16() for _ in range(2)]
+    sc = [0.01 + torch.rand(pages, page, HKV, generator=gen) for _ in range(2)] if e4m3 else [None, None]
+    own = torch.arange(pages, dtype=torch.int32).view(3, width)
+    both = own.clone()
+    both[1:, :shared] = own[0, :shared]  # one prefix for all
+    for t in (*raw, *sc):  # ... which the table without sharing holds three times
+        if t is not None:
+            t = t.view(torch.uint8) if e4m3 and t.dtype == dt else t
+            for i in (1, 2):
+                t[own[i, :shared].long()] = t[own[0, :shared].long()]
+    cu, lens = R.lens_to_cu(news).cuda(), torch.tensor(kv, dtype=torch.int32).cuda()
+    got = []
+    for table in (own, both):
+        kc, vc, ks, vs = (None if t is None else t.cuda() for t in (*raw, *sc))
+        before = [t.clone() for t in (kc, vc)]
+        tb = table.cuda()
+        g.gdn2_cache_write(k, v, kc, vc, cu, lens, tb, ks, vs)
+        o, lse = torch.full_like(q, 7.0), torch.full((n + tail, H), 7.0, device="cuda")
+        g.gdn2_attn_cached(q, kc, vc, cu, lens, tb, ks, vs, o=o, lse=lse)
+        kb, vb = torch.full_like(k, 7.0), torch.full_like(v, 7.0)
+        g.gdn2_cache_read(kc, vc, cu, lens, tb, ks, vs, k=kb, v=vb)
+        assert g.gdn2_sync_status() == 0
+        for t in (o, lse, kb, vb):
+            assert (t[n:] == 7).all() and torch.isfinite(t.float()).all()
+        written = torch.zeros(pages, page, dtype=torch.bool)
+        for i, m in enumerate(news):
+            for p in range(kv[i] - m, kv[i]):
+                written[table[i, p // page], p % page] = True
+        for x, y in zip((kc, vc), before):
+            same = (x.view(torch.uint8) == y.view(torch.uint8)).flatten(2).all(2).cpu()
+            assert same[~written].all() and not same[written].any()
+        got.append((o[:n], lse[:n], kb[:n], vb[:n]))
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
