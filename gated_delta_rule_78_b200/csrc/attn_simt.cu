@@ -37,6 +37,22 @@ __device__ __forceinline__ void load_tile(float *dst, const float *src, int rows
         *reinterpret_cast<float4 *>(dst + r * kStride<D> + c) = v;
     }
 }
+// the same by asynchronous copies, which the thread waits for itself
+template <int D, int n>
+__device__ __forceinline__ void fetch_tile(float *dst, const float *src, int rows, size_t stride, int tid, int threads)
+{
+    for (int i = tid; i < n * D / 4; i += threads) {
+        const int r = i / (D / 4), c = i % (D / 4) * 4;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst + r * kStride<D> + c)),
+                     "l"(r < rows ? src + (size_t)r * stride + c : src), "r"(r < rows ? 16 : 0)
+                     : "memory");
+    }
+}
+__device__ __forceinline__ void fetch_one(float *dst, const float *src, bool live)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 template <int n> __device__ __forceinline__ void group_sync(int group) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(n) : "memory"); }
 
 // acc[i][j] += A[4 ty + i] . B[tx + 16 j] over D channels
@@ -148,19 +164,22 @@ template <int D> __global__ void __launch_bounds__(Fwd<D>::NG * 4 * BQ) attn_fwd
     const size_t qs = (size_t)a.H * D, ks = (size_t)a.Hkv * D, qoff = (size_t)(r.sp.bos + q0) * qs + h * D;
     const float *k = (const float *)a.k + (size_t)r.sp.bos * ks + hk * D;
     const float *v = (const float *)a.v + (size_t)r.sp.bos * ks + hk * D;
+    const int last = min(q0 + BQ, len) - 1, jb = a.window == 0 || q0 < a.window ? 0 : (q0 - a.window + 1) / BC;
+    auto fetch = [&](float *dst, const float *src, int j) {
+        if (j * BC <= last) fetch_tile<D, BC>(dst, src + (size_t)j * BC * ks, len - j * BC, ks, tid, 4 * BQ);
+    };
+    fetch(K, k, jb + group);
     load_tile<D, BQ>(Q, (const float *)a.q + qoff, len - q0, qs, threadIdx.x, C::NG * 4 * BQ);
+    fetched();
     __syncthreads();
+    fetch(V, v, jb + group);
     float o[4][D / 16] = {}, m[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
     }
-    const int last = min(q0 + BQ, len) - 1, jb = a.window == 0 || q0 < a.window ? 0 : (q0 - a.window + 1) / BC;
-    for (int j = jb + group; j * BC <= last; j += C::NG) {
-        load_tile<D, BC>(K, k + (size_t)j * BC * ks, len - j * BC, ks, tid, 4 * BQ);
-        load_tile<D, BC>(V, v + (size_t)j * BC * ks, len - j * BC, ks, tid, 4 * BQ);
-        group_sync<4 * BQ>(group);
+    for (int j = jb + group; j * BC <= last; j += C::NG) {  // K is there, V on its way
         float s[4][4] = {};
         dot_tile<D>(s, Q, K, ty, tx);
 #pragma unroll
@@ -190,9 +209,13 @@ template <int D> __global__ void __launch_bounds__(Fwd<D>::NG * 4 * BQ) attn_fwd
 #pragma unroll
             for (int n = 0; n < D / 16; ++n) o[i][n] *= f;
         }
+        fetched();
         group_sync<4 * BQ>(group);
+        fetch(K, k, j + C::NG);
         mul_tile<D>(o, P, V, ty, tx);
+        fetched();
         group_sync<4 * BQ>(group);
+        fetch(V, v, j + C::NG);
     }
     // ---- the groups' sums joined
 #pragma unroll
@@ -252,6 +275,11 @@ template <int D> __global__ void __launch_bounds__(Dq<D>::NG * 4 * BQ) attn_dq_k
     const int h = blockIdx.y, hk = h / (a.H / a.Hkv), q0 = r.tile * BQ, len = r.sp.len;
     const size_t qs = (size_t)a.H * D, ks = (size_t)a.Hkv * D;
     const size_t qoff = (size_t)(r.sp.bos + q0) * qs + h * D, koff = (size_t)r.sp.bos * ks + hk * D;
+    const int last = min(q0 + BQ, len) - 1, jb = a.window == 0 || q0 < a.window ? 0 : (q0 - a.window + 1) / BC;
+    auto fetch = [&](float *dst, const void *src, int j) {
+        if (j * BC <= last) fetch_tile<D, BC>(dst, (const float *)src + koff + (size_t)j * BC * ks, len - j * BC, ks, tid, 4 * BQ);
+    };
+    fetch(V, a.v, jb + group);
     load_tile<D, BQ>(Q, (const float *)a.q + qoff, len - q0, qs, threadIdx.x, C::NG * 4 * BQ);
     load_tile<D, BQ>(O, (const float *)a.d_o + qoff, len - q0, qs, threadIdx.x, C::NG * 4 * BQ);
     float lse[4], delta[4];
@@ -262,16 +290,17 @@ template <int D> __global__ void __launch_bounds__(Dq<D>::NG * 4 * BQ) attn_dq_k
         lse[i] = row < len ? a.lse[at] : 0.f;
         delta[i] = row < len ? a.delta[at] : 0.f;
     }
+    fetched();
     __syncthreads();
+    fetch(K, a.k, jb + group);
     float dq[4][D / 16] = {};
-    const int last = min(q0 + BQ, len) - 1, jb = a.window == 0 || q0 < a.window ? 0 : (q0 - a.window + 1) / BC;
-    for (int j = jb + group; j * BC <= last; j += C::NG) {
-        load_tile<D, BC>(K, (const float *)a.k + koff + (size_t)j * BC * ks, len - j * BC, ks, tid, 4 * BQ);
-        load_tile<D, BC>(V, (const float *)a.v + koff + (size_t)j * BC * ks, len - j * BC, ks, tid, 4 * BQ);
-        group_sync<4 * BQ>(group);
+    for (int j = jb + group; j * BC <= last; j += C::NG) {  // V is there, K on its way
         float s[4][4] = {}, dp[4][4] = {};
-        dot_tile<D>(s, Q, K, ty, tx);
         dot_tile<D>(dp, O, V, ty, tx);
+        fetched();
+        group_sync<4 * BQ>(group);
+        fetch(V, a.v, j + C::NG);
+        dot_tile<D>(s, Q, K, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -281,7 +310,9 @@ template <int D> __global__ void __launch_bounds__(Dq<D>::NG * 4 * BQ) attn_dq_k
             }
         group_sync<4 * BQ>(group);
         mul_tile<D>(dq, S, K, ty, tx);
+        fetched();
         group_sync<4 * BQ>(group);
+        fetch(K, a.k, j + C::NG);
     }
     put_sums<D>(mine, dq, ty, tx);
     __syncthreads();
@@ -301,26 +332,35 @@ template <int D, int BK> __global__ void __launch_bounds__(Dkv<D, BK>::NG * 4 * 
     const int hk = blockIdx.y, heads = a.H / a.Hkv, k0 = r.tile * BK, len = r.sp.len;
     const size_t qs = (size_t)a.H * D, ks = (size_t)a.Hkv * D;
     const size_t koff = (size_t)(r.sp.bos + k0) * ks + hk * D;
-    load_tile<D, BK>(K, (const float *)a.k + koff, len - k0, ks, threadIdx.x, C::NG * 4 * BK);
-    load_tile<D, BK>(V, (const float *)a.v + koff, len - k0, ks, threadIdx.x, C::NG * 4 * BK);
-    __syncthreads();
-    float dk[4][D / 16] = {}, dv[4][D / 16] = {};
     // queries k0 .. the last that still sees the tile's last key
     const int end = a.window == 0 || a.window > len ? len : min(len, k0 + BK - 1 + a.window), tiles = (end - k0 + BC - 1) / BC;
-    for (int i = group; i < heads * tiles; i += C::NG) {
+    auto fetch = [&](float *dst, const void *src, int i) {
+        if (i >= heads * tiles) return;
         const int h = hk * heads + i / tiles, q0 = k0 + i % tiles * BC;
-        const size_t qoff = (size_t)(r.sp.bos + q0) * qs + h * D;
-        load_tile<D, BC>(Q, (const float *)a.q + qoff, len - q0, qs, tid, 4 * BK);
-        load_tile<D, BC>(O, (const float *)a.d_o + qoff, len - q0, qs, tid, 4 * BK);
-        if (tid < BC) {
-            const size_t at = (size_t)(r.sp.bos + q0 + tid) * a.H + h;
-            lse[tid] = q0 + tid < len ? a.lse[at] : 0.f;
-            delta[tid] = q0 + tid < len ? a.delta[at] : 0.f;
-        }
-        group_sync<4 * BK>(group);
+        fetch_tile<D, BC>(dst, (const float *)src + (size_t)(r.sp.bos + q0) * qs + h * D, len - q0, qs, tid, 4 * BK);
+    };
+    auto fetch_stats = [&](int i) {
+        if (i >= heads * tiles || tid >= BC) return;
+        const int h = hk * heads + i / tiles, q = k0 + i % tiles * BC + tid;
+        const size_t at = (size_t)(r.sp.bos + min(q, len - 1)) * a.H + h;
+        fetch_one(lse + tid, a.lse + at, q < len);
+        fetch_one(delta + tid, a.delta + at, q < len);
+    };
+    fetch(O, a.d_o, group);
+    fetch_stats(group);
+    load_tile<D, BK>(K, (const float *)a.k + koff, len - k0, ks, threadIdx.x, C::NG * 4 * BK);
+    load_tile<D, BK>(V, (const float *)a.v + koff, len - k0, ks, threadIdx.x, C::NG * 4 * BK);
+    fetched();
+    __syncthreads();
+    fetch(Q, a.q, group);
+    float dk[4][D / 16] = {}, dv[4][D / 16] = {};
+    for (int i = group; i < heads * tiles; i += C::NG) {  // O, lse and delta are there, Q on its way
+        const int q0 = k0 + i % tiles * BC;
         float s[4][4] = {}, dp[4][4] = {};
-        dot_tile<D>(s, K, Q, ty, tx);
         dot_tile<D>(dp, V, O, ty, tx);
+        fetched();
+        group_sync<4 * BK>(group);
+        dot_tile<D>(s, K, Q, ty, tx);
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -333,8 +373,13 @@ template <int D, int BK> __global__ void __launch_bounds__(Dkv<D, BK>::NG * 4 * 
             }
         group_sync<4 * BK>(group);
         mul_tile<D>(dv, P, O, ty, tx);
-        mul_tile<D>(dk, S, Q, ty, tx);
         group_sync<4 * BK>(group);
+        fetch(O, a.d_o, i + C::NG);
+        fetch_stats(i + C::NG);
+        mul_tile<D>(dk, S, Q, ty, tx);
+        fetched();
+        group_sync<4 * BK>(group);
+        fetch(Q, a.q, i + C::NG);
     }
     put_sums<D>(mine, dk, ty, tx);
     put_sums<D>(mine + BK * D, dv, ty, tx);
