@@ -8,13 +8,14 @@
 // A block owns 32 queries, or for dk and dv 16 or 32 keys, and walks over the other side in tiles of 64.  Its
 // groups of 4 threads to a row take the tiles in turn, each with shared memory of its own, and add up at
 // the end, in order: an fp32 batch is mostly a small one, whose few blocks would otherwise leave an SM two
-// warps to a scheduler.  A thread forms 4 x 4 scores and 4 rows x D / 16 channels of each product, with
-// 16-byte loads of both operands from shared memory: 12 wavefronts of them to 64 FMAs of a warp, so
-// bound by the FP32 pipe first and shared memory next.  The backward runs two kernels, so that no sum
-// depends on the order in which blocks run.
+// warps to a scheduler.  The next tile's loads run behind this one's arithmetic, each as soon as its buffer
+// is free.  A thread forms 4 x 4 scores and 4 rows x D / 16 channels of each product, two values to an
+// instruction, with 16-byte loads of both operands from shared memory: 12 wavefronts of them to 32 pairs of
+// FMAs of a warp, 16 of its scheduler's cycles, so bound by both pipes at once.  The backward runs two kernels,
+// so that no sum depends on the order in which blocks run.
 //
-// 2 x 500 tokens, 4 heads on 2, D = 64: forward 28 us, delta 2, dk and dv 48, dq 31.  At such sizes a block's
-// few tiles one after another are the time, and in a tile the loads, for which nothing else is ready.
+// 2 x 500 tokens, 4 heads on 2, D = 64: forward 24 us, delta 2, dk and dv 45, dq 30: a block's two or three tiles
+// one after another.  8 x 2048, 16 heads, D = 128: forward 4.5 ms, 31 TFLOP/s, backward 13.8 ms.
 #include "attn.cuh"
 
 namespace gdn2 {
@@ -55,33 +56,42 @@ __device__ __forceinline__ void fetch_one(float *dst, const float *src, bool liv
 __device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 template <int n> __device__ __forceinline__ void group_sync(int group) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "n"(n) : "memory"); }
 
-// acc[i][j] += A[4 ty + i] . B[tx + 16 j] over D channels
+// acc[i][j] = A[4 ty + i] . B[tx + 16 j] over D channels: even and odd ones in the halves of a pair
 template <int D>
 __device__ __forceinline__ void dot_tile(float (&acc)[4][4], const float *A, const float *B, int ty, int tx)
 {
+    uint64_t sum[4][4] = {};
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
-        float4 x[4], y[4];
+        ulonglong2 x[4], y[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(A + (4 * ty + i) * kStride<D> + c);
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const ulonglong2 *>(A + (4 * ty + i) * kStride<D> + c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(B + (tx + 16 * j) * kStride<D> + c);
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const ulonglong2 *>(B + (tx + 16 * j) * kStride<D> + c);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
-                acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
-                acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
-                acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
-            }
+            for (int j = 0; j < 4; ++j) sum[i][j] = fma2(x[i].y, y[j].y, fma2(x[i].x, y[j].x, sum[i][j]));
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float lo, hi;
+            unpair(sum[i][j], lo, hi);
+            acc[i][j] = lo + hi;
+        }
 }
 
 // acc[i][n] += sum over the 64 columns t of P[4 ty + i][t] * X[t][64 (n / 4) + 4 tx + n % 4]
 template <int D>
 __device__ __forceinline__ void mul_tile(float (&acc)[4][D / 16], const float *P, const float *X, int ty, int tx)
 {
+    uint64_t sum[4][D / 32];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n) sum[i][n] = pair(acc[i][2 * n], acc[i][2 * n + 1]);
 #pragma unroll 2
     for (int t = 0; t < BC; t += 4) {
         float p[4][4];
@@ -91,16 +101,19 @@ __device__ __forceinline__ void mul_tile(float (&acc)[4][D / 16], const float *P
         for (int z = 0; z < 4; ++z)
 #pragma unroll
             for (int n = 0; n < D / 64; ++n) {
-                const float4 x = *reinterpret_cast<const float4 *>(X + (t + z) * kStride<D> + 64 * n + 4 * tx);
+                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(X + (t + z) * kStride<D> + 64 * n + 4 * tx);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    acc[i][4 * n] = fmaf(p[i][z], x.x, acc[i][4 * n]);
-                    acc[i][4 * n + 1] = fmaf(p[i][z], x.y, acc[i][4 * n + 1]);
-                    acc[i][4 * n + 2] = fmaf(p[i][z], x.z, acc[i][4 * n + 2]);
-                    acc[i][4 * n + 3] = fmaf(p[i][z], x.w, acc[i][4 * n + 3]);
+                    const uint64_t p2 = pair(p[i][z], p[i][z]);
+                    sum[i][2 * n] = fma2(p2, x.x, sum[i][2 * n]);
+                    sum[i][2 * n + 1] = fma2(p2, x.y, sum[i][2 * n + 1]);
                 }
             }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < D / 32; ++n) unpair(sum[i][n], acc[i][2 * n], acc[i][2 * n + 1]);
 }
 
 __device__ __forceinline__ bool visible(int i, int j, int len, int window)
@@ -180,7 +193,7 @@ template <int D> __global__ void __launch_bounds__(Fwd<D>::NG * 4 * BQ) attn_fwd
         l[i] = 0.f;
     }
     for (int j = jb + group; j * BC <= last; j += C::NG) {  // K is there, V on its way
-        float s[4][4] = {};
+        float s[4][4];
         dot_tile<D>(s, Q, K, ty, tx);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -295,7 +308,7 @@ template <int D> __global__ void __launch_bounds__(Dq<D>::NG * 4 * BQ) attn_dq_k
     fetch(K, a.k, jb + group);
     float dq[4][D / 16] = {};
     for (int j = jb + group; j * BC <= last; j += C::NG) {  // V is there, K on its way
-        float s[4][4] = {}, dp[4][4] = {};
+        float s[4][4], dp[4][4];
         dot_tile<D>(dp, O, V, ty, tx);
         fetched();
         group_sync<4 * BQ>(group);
@@ -356,7 +369,7 @@ template <int D, int BK> __global__ void __launch_bounds__(Dkv<D, BK>::NG * 4 * 
     float dk[4][D / 16] = {}, dv[4][D / 16] = {};
     for (int i = group; i < heads * tiles; i += C::NG) {  // O, lse and delta are there, Q on its way
         const int q0 = k0 + i % tiles * BC;
-        float s[4][4] = {}, dp[4][4] = {};
+        float s[4][4], dp[4][4];
         dot_tile<D>(dp, V, O, ty, tx);
         fetched();
         group_sync<4 * BK>(group);
@@ -402,8 +415,8 @@ template <int D, int BK> cudaError_t run_dkv(const AttnArgs &a, cudaStream_t s)
 }
 template <int D> cudaError_t run_bwd(const AttnArgs &a, cudaStream_t s)
 {
-    // 16 keys to a block where 32 would not fill the SMs twice (2 x 500, 2 key heads, d 64: 48 us against
-    // 88); else 32, which read each query tile half as often (8 x 2048, 16 heads, d 128: 15.3 ms against 19.7)
+    // 16 keys to a block where 32 would not fill the SMs twice (2 x 500, 2 key heads, d 64: dk and dv 45 us against
+    // 76); else 32, which read each query tile half as often (8 x 2048, 16 heads, d 128: 13.8 ms against 17.3)
     const bool few = tile_bound(a.b, 32) * a.Hkv < 2LL * device_sms();
     cudaError_t e = few ? run_dkv<D, 16>(a, s) : run_dkv<D, 32>(a, s);
     const dim3 grid((unsigned)tile_bound(a.b, BQ), (unsigned)a.H);
