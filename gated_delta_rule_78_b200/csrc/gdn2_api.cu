@@ -14,7 +14,7 @@ cudaError_t set_smem_attr(const void *kernel, int bytes)
 {
     // (kernel, device) pairs already raised; a small table is enough for the handful of kernels here
     struct Entry { const void *fn; uint64_t devices; };
-    static Entry table[32];
+    static Entry table[64];
     static std::mutex mu;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -22,7 +22,7 @@ cudaError_t set_smem_attr(const void *kernel, int bytes)
     if (dev < 0 || dev >= 64) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     std::lock_guard<std::mutex> lock(mu);
     int slot = -1;
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < 64; ++i) {
         if (table[i].fn == kernel) { slot = i; break; }
         if (!table[i].fn && slot < 0) slot = i;
     }
