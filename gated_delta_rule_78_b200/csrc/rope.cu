@@ -16,7 +16,7 @@
 // The angle is formed and reduced modulo 2 pi in 64 bits: pos * inv_freq in fp32 would be off by
 // 2^-24 of an angle of up to 10^5.
 //
-// 32768 tokens, 16 + 16 heads, D = 128, bf16: forward 103 us (5.2 TB/s), backward 176 us (4.6 TB/s) and 6 us
+// 32768 tokens, 16 + 16 heads, D = 128, bf16: forward 102 us (5.3 TB/s), backward 174 us (4.6 TB/s) and 3 us
 // for the weights' sums.  The rest to the copy rate is the norm's two dependent passes over registers, and in the
 // backward the registers of four rows of x and dy, which leave two blocks to an SM.
 #include "attn.cuh"
@@ -288,19 +288,32 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float *partial, int
     if (threadIdx.x == 0 && dst) dst[blockIdx.x * 32 + threadIdx.y] = v;
 }
 
-// Many tokens: a few of them to a warp, six blocks to an SM (two or three run at a time).
-unsigned rope_grid(long long n)
+// Many tokens: as many blocks as run at once (`per` to an SM), so that none starts late (32768 tokens, bf16: three
+// and two blocks to an SM 102 and 171 us, six 104 and 177, a warp to a token 112 and 204).
+unsigned rope_grid(long long n, int per)
 {
-    const long long want = n < kShareBelow ? n : (n + kWarps - 1) / kWarps, most = (long long)device_sms() * 6;
+    if (n < kShareBelow) return (unsigned)n;
+    const long long want = (n + kWarps - 1) / kWarps, most = (long long)device_sms() * per;
     return (unsigned)(want < most ? want : most);
 }
+constexpr int kBwdPerSm = 2;  // of every backward kernel, and the rows of the weight gradients' partial sums
 
-template <typename T, int D, bool bwd> void run(const RopeArgs &a, unsigned grid, cudaStream_t s)
+template <typename T, int D, int mode, bool bwd> cudaError_t run(const RopeArgs &a, cudaStream_t s)
+{
+    auto kernel = rope_kernel<T, D, mode, bwd>;
+    static const int per = [&] {
+        int n = 0;
+        if (bwd || cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kWarps * 32, 0) != cudaSuccess || n < 1) n = kBwdPerSm;
+        return n;
+    }();
+    kernel<<<rope_grid(a.n, per), kWarps * 32, 0, s>>>(a);
+    return cudaGetLastError();
+}
+template <typename T, int D, bool bwd> cudaError_t run(const RopeArgs &a, cudaStream_t s)
 {
     const int half = a.rot >> 1;
-    if (a.interleaved || a.rot == 0) rope_kernel<T, D, kPair, bwd><<<grid, kWarps * 32, 0, s>>>(a);
-    else if (half % kVec<T> == 0) rope_kernel<T, D, kSwap, bwd><<<grid, kWarps * 32, 0, s>>>(a);
-    else rope_kernel<T, D, kAny, bwd><<<grid, kWarps * 32, 0, s>>>(a);
+    if (a.interleaved || a.rot == 0) return run<T, D, kPair, bwd>(a, s);
+    return half % kVec<T> == 0 ? run<T, D, kSwap, bwd>(a, s) : run<T, D, kAny, bwd>(a, s);
 }
 
 }  // namespace
@@ -315,20 +328,20 @@ int device_sms()
     return sms;
 }
 
-int rope_bwd_blocks(long long n) { return n > 0 ? (int)rope_grid(n) : 0; }
+int rope_bwd_blocks(long long n) { return n > 0 ? (int)rope_grid(n, kBwdPerSm) : 0; }
 
 cudaError_t launch_rope(bool bwd, bool fp32, const RopeArgs &a, cudaStream_t s)
 {
-    const unsigned grid = rope_grid(a.n);
+    cudaError_t e;
     if (a.D == 128) {
-        if (fp32) bwd ? run<float, 128, true>(a, grid, s) : run<float, 128, false>(a, grid, s);
-        else bwd ? run<__nv_bfloat16, 128, true>(a, grid, s) : run<__nv_bfloat16, 128, false>(a, grid, s);
+        if (fp32) e = bwd ? run<float, 128, true>(a, s) : run<float, 128, false>(a, s);
+        else e = bwd ? run<__nv_bfloat16, 128, true>(a, s) : run<__nv_bfloat16, 128, false>(a, s);
     } else {
-        if (fp32) bwd ? run<float, 64, true>(a, grid, s) : run<float, 64, false>(a, grid, s);
-        else bwd ? run<__nv_bfloat16, 64, true>(a, grid, s) : run<__nv_bfloat16, 64, false>(a, grid, s);
+        if (fp32) e = bwd ? run<float, 64, true>(a, s) : run<float, 64, false>(a, s);
+        else e = bwd ? run<__nv_bfloat16, 64, true>(a, s) : run<__nv_bfloat16, 64, false>(a, s);
     }
-    if (bwd && a.partial)
-        rope_dw_kernel<<<dim3(a.D / 32, 2), dim3(32, 32), 0, s>>>(a.partial, (int)grid, a.D, a.dwq, a.dwk);
+    if (e != cudaSuccess || !bwd || !a.partial) return e;
+    rope_dw_kernel<<<dim3(a.D / 32, 2), dim3(32, 32), 0, s>>>(a.partial, rope_bwd_blocks(a.n), a.D, a.dwq, a.dwk);
     return cudaGetLastError();
 }
 
