@@ -16,7 +16,7 @@
 // The angle is formed and reduced modulo 2 pi in 64 bits: pos * inv_freq in fp32 would be off by
 // 2^-24 of an angle of up to 10^5.
 //
-// 32768 tokens, 16 + 16 heads, D = 128, bf16: forward 102 us (5.3 TB/s), backward 174 us (4.6 TB/s) and 3 us
+// 32768 tokens, 16 + 16 heads, D = 128, bf16: forward 101 us (5.3 TB/s), backward 173 us (4.7 TB/s) and 3 us
 // for the weights' sums.  The rest to the copy rate is the norm's two dependent passes over registers, and in the
 // backward the registers of four rows of x and dy, which leave two blocks to an SM.
 #include "attn.cuh"
