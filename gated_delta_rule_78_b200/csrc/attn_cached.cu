@@ -448,6 +448,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // the joining kernel may be brought to the SMs; it waits there for this one's end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // ---- the warps' sums joined: O and (m, l) of each warp over the rings
     __syncthreads();
     float *so = reinterpret_cast<float *>(sm);
@@ -518,6 +520,7 @@ template <int D, int W> __global__ void __launch_bounds__(256) attn_join_kernel(
 {
     constexpr int E = D / 32, kAhead = 4;
     __shared__ float s_top[8], s_sum[8], s_acc[W > 1 ? 8 : 1][D];
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for all of the parts
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = W > 1 ? warp : 0;
     const long long at = W > 1 ? blockIdx.x : (long long)blockIdx.x * 8 + warp;
     const long long n = p.b.rows * p.H;
@@ -687,8 +690,19 @@ cudaError_t launch_attn_cached(const CachedArgs &a, bool use_tc, cudaStream_t s)
     const long long rows = a.b.rows * a.H;
     // 8 warps to a row where parts are many and rows too few to fill the SMs (16 rows, 37 parts: 24 us in all,
     // a warp to a row 38; 2048 rows, 16 parts: 52 and 50; 32768 rows: 454 and 379)
-    if (a.splits > 8 && rows <= kManyRows) (a.D == 128 ? attn_join_kernel<128, 8> : attn_join_kernel<64, 8>)<<<(unsigned)rows, 256, 0, s>>>(p);
-    else (a.D == 128 ? attn_join_kernel<128, 1> : attn_join_kernel<64, 1>)<<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(p);
+    const bool wide = a.splits > 8 && rows <= kManyRows;
+    cudaLaunchAttribute early;  // launched while the last parts are written: one sequence over 32768 keys 2 us sooner
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(wide ? rows : (rows + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    if (wide) e = a.D == 128 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<128, 8>, p) : cudaLaunchKernelEx(&cfg, attn_join_kernel<64, 8>, p);
+    else e = a.D == 128 ? cudaLaunchKernelEx(&cfg, attn_join_kernel<128, 1>, p) : cudaLaunchKernelEx(&cfg, attn_join_kernel<64, 1>, p);
+    if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 
