@@ -164,11 +164,12 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
     if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 0) report_bad_seqlens(p.b, p.status);
     TileRef r;
     if (!find_rows(p, blockIdx.x, kRows, r)) return;
-    const int kvlen = p.c.kv_lens[r.seq], first = kvlen - r.sp.len;
-    if (first < 0 || kvlen > (long long)p.c.width * p.c.page) {
+    const int kvlen = p.c.kv_lens[r.seq];
+    if (kvlen < r.sp.len || kvlen > (long long)p.c.width * p.c.page) {  // before any difference, which could wrap
         if (tid == 0) atomicExch(p.status, kStatusBadPages);
         return;
     }
+    const int first = kvlen - r.sp.len;
     const int hk = blockIdx.y, r0 = r.tile * kRows, rows = min(kRows, r.sp.len * p.G - r0);
     // keys that this tile's rows see, and this block's part of them
     const int low = first + r0 / p.G, high = first + (r0 + rows - 1) / p.G;
@@ -179,8 +180,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_rows_kernel(const __grid_con
         const int rr = r0 + row, tok = rr / p.G;
         return (size_t)(r.sp.bos + tok) * p.H + hk * p.G + (rr - tok * p.G);
     };
-    if (kb >= ke) {  // nothing in this part
-        if (tid < rows) p.part_l[part + row_at(tid)] = -INFINITY;
+    if (kb >= ke) {  // nothing in this part (one part alone has keys: part_l may be null then)
+        if (p.splits > 1 && tid < rows) p.part_l[part + row_at(tid)] = -INFINITY;
         return;
     }
 

@@ -246,3 +246,37 @@ def test_repeatable_and_graphs(cuda_lib, e4m3):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+@pytest.mark.parametrize("rows,capacity", [(1, 160), (1, 4096), (70, 160), (70, 4096)])
+def test_lengths_far_below_zero(cuda_lib, rows, capacity, e4m3):
+    """A length whose difference to the new tokens wraps in 32 bits skips the sequence as any other below
+    them does, in one part (no workspace) and in several, few rows and many."""
+    g = cuda_lib
+    for bad in (-2 ** 31, -2 ** 31 + rows - 1, -2 ** 31 + rows, -1, rows - 1):
+        b = Batch([rows, rows], [rows + 40, rows + 50], 16, 2, 64, e4m3, seed=3).fill(g)
+        d = b.dev
+        wide = torch.full((2, capacity // 16), -5, dtype=torch.int32)
+        wide[:, :b.table.shape[1]] = b.table[:, :capacity // 16]
+        d["table"] = wide.cuda()
+        q = torch.randn(b.total, 4, 64).bfloat16().cuda()
+        good, good_lse = g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args())
+        assert g.gdn2_sync_status() == 0
+        d["kv"][1] = bad
+        o, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+        g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args(), o=o, lse=lse)
+        assert g.gdn2_sync_status() == -11, bad
+        assert torch.equal(o[:rows], good[:rows]) and torch.equal(lse[:rows], good_lse[:rows])
+        assert (o[rows:] == 7.0).all() and (lse[rows:] == 7.0).all()
+        k, v = (torch.full((b.total, 2, 64), 7.0).bfloat16().cuda() for _ in range(2))
+        g.gdn2_cache_read(d["kc"], d["vc"], *b.args(), k=k, v=v)
+        assert g.gdn2_sync_status() == -11, bad
+        assert (k[rows:] == 7.0).all() and (v[rows:] == 7.0).all() and (k[:rows] != 7.0).any()
+        before = d["kc"].view(torch.uint8).clone()
+        g.gdn2_cache_write(k, k, d["kc"], d["vc"], *b.args())
+        assert g.gdn2_sync_status() == -11, bad
+        changed = (before != d["kc"].view(torch.uint8)).flatten(2).any(-1).flatten()
+        first = b.kv[0] - rows
+        own = {int(b.table[0, p // 16]) * 16 + p % 16 for p in range(first, b.kv[0])}
+        assert set(changed.nonzero().flatten().tolist()) <= own
