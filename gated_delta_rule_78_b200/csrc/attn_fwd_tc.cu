@@ -88,6 +88,7 @@ struct FwdParams {
 // The key tiles that a block works on, and each query tile's share of them.
 struct Ranges {
     int first, kvlen;        // position of the sequence's query token 0; keys
+    int least;               // the first key that a query of the block sees: pages wholly before it may be another's by now
     int t0[2], n[2];         // first token of tile A / B in the sequence, tokens in it
     int beg[2], end[2];      // its key tiles
     int jb, je;              // their union
@@ -97,6 +98,7 @@ __device__ __forceinline__ Ranges make_ranges(const FwdParams &p, const TileRef 
     Ranges g;
     g.kvlen = kvlen;
     g.first = kvlen - r.sp.len;
+    g.least = p.window ? max(0, g.first + 2 * r.tile * p.TQ - p.window + 1) : 0;
     int lo = INT_MAX, hi = 0;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -476,9 +478,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_tc_kernel(const __grid_c
                 const int seg = lane / C::NB, blk = lane % C::NB, off = blk * kBoxBytes + seg * p.box * 128;
                 const bool live = seg * p.box < kBN;
                 const int *table = p.c.table + (size_t)r.seq * p.c.width;
-                auto row_of = [&](int j) {  // its row in the cache, past the end (zeros) for what the sequence lacks
+                // its row in the cache, past the end (zeros) for what the sequence lacks or the window has left behind
+                auto row_of = [&](int j) {
                     const int at = j * kBN + seg * p.box, none = p.c.num_pages * p.c.page;
-                    if (!live || at >= g.kvlen) return none;
+                    if (!live || at >= g.kvlen || at + p.box <= g.least) return none;
                     const int pg = at / p.c.page, id = table[pg];
                     if (id >= 0 && id < p.c.num_pages) return id * p.c.page + (at - pg * p.c.page);
                     atomicExch(p.status, kStatusBadPages);
@@ -516,13 +519,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_tc_kernel(const __grid_c
                 const int *table = p.c.table + (size_t)r.seq * p.c.width;
                 constexpr int CH = e4m3 ? D / 16 : D / 8, RP = 32 / CH;  // 16-byte chunks of a row, rows a pass
                 const int ch = lane % CH;
-                // rows lane + 32 i of a key tile: their slots in the cache, -1 past the sequence
+                // rows lane + 32 i of a key tile: their slots in the cache, -1 past the sequence and before the window
                 auto find_slots = [&](int j, int (&slot)[4]) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int at = j * kBN + 32 * i + lane;
                         slot[i] = -1;
-                        if (at >= g.kvlen) continue;
+                        if (at >= g.kvlen || at < g.least) continue;
                         const int pg = at / p.c.page, id = table[pg];
                         if (id >= 0 && id < p.c.num_pages) slot[i] = id * p.c.page + (at - pg * p.c.page);
                         else atomicExch(p.status, kStatusBadPages);

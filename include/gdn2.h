@@ -397,7 +397,8 @@ GDN2_API size_t gdn2_attn_workspace_size(gdn2_dtype dt, int N, int T, int H, int
  * The paged cache.  k_cache, v_cache: [num_pages, page_size, Hkv, D], bf16 or e4m3 (one byte); e4m3
  * has fp32 scales [num_pages, page_size, Hkv] for keys and for values.
  *   block_table: DEVICE int32 [N, max_pages]; position p of sequence n is row p % page_size of page
- *                block_table[n][p / page_size].  Entries past a sequence's length are not read.
+ *                block_table[n][p / page_size].  Entries past a sequence's length are not read, nor, by
+ *                attention with a window, those of pages wholly before the first key that its new tokens see.
  *   kv_lens:     DEVICE int32 [N], the sequence's length WITH its new tokens: the rows that
  *                cu_seqlens gives sequence n are its positions kv_lens[n] - (c_{n+1} - c_n) ..
  *                kv_lens[n] - 1.

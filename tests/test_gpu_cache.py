@@ -280,3 +280,30 @@ def test_lengths_far_below_zero(cuda_lib, rows, capacity, e4m3):
         first = b.kv[0] - rows
         own = {int(b.table[0, p // 16]) * 16 + p % 16 for p in range(first, b.kv[0])}
         assert set(changed.nonzero().flatten().tolist()) <= own
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("page,rows,window", [(1, 1, 40), (16, 1, 40), (1, 150, 40), (7, 150, 100), (8, 150, 100), (16, 300, 1),
+                                              (64, 150, 20), (256, 150, 20)])
+def test_pages_behind_the_window(cuda_lib, page, rows, window, D, e4m3):
+    """Pages that no query sees any more (a server frees them) are not looked up: their entries may be no
+    page, or one that has become another sequence's, NaN among its values."""
+    g = cuda_lib
+    b = Batch([rows, rows], [rows + 700, rows + 515], page, 2, D, e4m3, seed=page + rows).fill(g)
+    d = b.dev
+    q = torch.randn(b.total, 4, D, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    want = g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args(), window=window)
+    assert g.gdn2_sync_status() == 0
+    poison = min(set(range(b.kc.shape[0])) - set(b.table.flatten().tolist()))  # of no sequence: still all NaN
+    for entry in (-1, b.kc.shape[0], poison):
+        table = b.table.clone()
+        for i, kv in enumerate(b.kv):
+            gone = max(0, kv - rows - window + 1) // page
+            assert gone > 0 or page == 256
+            table[i, :gone] = entry
+        d["table"] = table.cuda()
+        got = g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args(), window=window)
+        assert g.gdn2_sync_status() == 0, entry
+        for x, y in zip(got, want):
+            assert torch.equal(x, y), entry
