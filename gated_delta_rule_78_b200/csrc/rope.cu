@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kWarps * 32, bwd ? 2 : 3) rope_kernel(const Ro
 #pragma unroll
                         for (int m = L / 2; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
                         r = rsqrtf(ss * (1.f / D) + a.eps);
+                        if (bwd && h >= heads) r = 0.f;  // zeros past the heads: not 0 * inf in dw where eps is 0
                     }
                     const uint64_t r2 = pair(r, r);
                     if constexpr (!bwd) {

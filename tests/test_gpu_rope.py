@@ -163,3 +163,11 @@ def test_weight_gradient_is_repeatable_and_graphs(cuda_lib):
     torch.cuda.synchronize()
     for n in a:
         assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,Hkv", [(1, 3), (16, 5)])
+def test_no_eps(cuda_lib, H, Hkv, dt):
+    """eps 0 is allowed: passes that end past the last head add nothing to the weights' gradients."""
+    x = make(40, H, Hkv, 128, 128, dt, seed=H)
+    verify(x, 1, run(cuda_lib, x, 1, eps=0.0), eps=0.0)
