@@ -239,14 +239,14 @@ __global__ void __launch_bounds__(kWarps * 32, bwd ? 2 : 3) rope_kernel(const Ro
                                 d2 = fma2(ux, wt[e], d2);
                             }
                         }
-                        if (a.norm) {  // dx = u (r w) - x (r^3 / D sum u w x)
+                        if (a.norm) {  // dx = r (u w - x (r^2 / D sum u w x)): r^3 leaves fp32's range where r does not
                             float dot = sum_of(d2);
 #pragma unroll
                             for (int m = L / 2; m >= 1; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-                            dot *= -r * r * r * (1.f / D);
+                            dot *= -r * r * (1.f / D);
                             const uint64_t k2 = pair(dot, dot);
 #pragma unroll
-                            for (int e = 0; e < P; ++e) u2[e] = fma2(u2[e], mul2(wt[e], r2), mul2(f[e], k2));
+                            for (int e = 0; e < P; ++e) u2[e] = mul2(fma2(f[e], k2, mul2(u2[e], wt[e])), r2);
                         }
                         if (h < heads) *reinterpret_cast<uint4 *>(y + (size_t)h * D) = pack(u2);
                     }

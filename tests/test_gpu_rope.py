@@ -171,3 +171,14 @@ def test_no_eps(cuda_lib, H, Hkv, dt):
     """eps 0 is allowed: passes that end past the last head add nothing to the weights' gradients."""
     x = make(40, H, Hkv, 128, 128, dt, seed=H)
     verify(x, 1, run(cuda_lib, x, 1, eps=0.0), eps=0.0)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("flags", [1, 3])
+def test_far_scales_without_eps(cuda_lib, flags, dt):
+    """Rows of 1e15 to 1e-16 with eps 0: 1 / rms goes from 1e-15 to 1e16, whose cubes fp32 does not hold."""
+    x = make(9, 2, 1, 64, 64, torch.float32, seed=11)
+    for n in ("q", "k"):
+        x[n] *= torch.logspace(15, -16, 9)[:, None, None]
+    x = {n: t.to(dt) if n in ("q", "k", "dq", "dk") else t for n, t in x.items()}
+    verify(x, flags, run(cuda_lib, x, flags, eps=0.0), eps=0.0)
