@@ -36,4 +36,4 @@ from ._lib import (EXPORTS, GDN2_BF16, GDN2_F32, GDN2_OK, LIB_PATH, NOALLOC_MAX_
 from ._attn import (CACHE_BF16, CACHE_E4M3, ROPE_INTERLEAVED, ROPE_RMSNORM, gdn2_attn_bwd,  # noqa: F401
                     gdn2_attn_bwd_varlen, gdn2_attn_cached, gdn2_attn_cached_workspace_size, gdn2_attn_fwd,
                     gdn2_attn_fwd_varlen, gdn2_attn_workspace_size, gdn2_cache_read, gdn2_cache_write, gdn2_qk_rope,
-                    gdn2_qk_rope_bwd)
+                    gdn2_qk_rope_bwd, gdn2_qk_rope_workspace_size)

@@ -149,6 +149,11 @@ def gdn2_qk_rope_bwd(q, k, q_weight, k_weight, positions, inv_freq, d_q_out, d_k
     return out
 
 
+def gdn2_qk_rope_workspace_size(dtype, N: int, H: int, Hkv: int, D: int, flags: int = ROPE_RMSNORM) -> int:
+    """Bytes of gdn2_qk_rope_bwd's workspace for up to N rows (0 without ROPE_RMSNORM: none is needed)."""
+    return int(raw().gdn2_qk_rope_workspace_size(flags, GDN2_F32 if dtype == torch.float32 else GDN2_BF16, N, H, Hkv, D))
+
+
 # ------------------------------------------------------------------ attention over whole sequences
 def _attn_args(q, k, v, cu_seqlens):
     dev, dtype, qs, ks = _device(q), q.dtype, q.shape, k.shape

@@ -219,7 +219,8 @@ struct RopeArgs {
     void *dq, *dk;               // backward outputs
     float *dwq, *dwk, *partial;  // backward weight gradients and their per-block sums
 };
-int rope_bwd_blocks(long long n);
+int rope_bwd_blocks(long long n);       // of n token rows' backward pass, a row of `partial` each
+int rope_bwd_most_blocks(long long n);  // ... of any pass of up to n token rows
 cudaError_t launch_rope(bool bwd, bool fp32, const RopeArgs &a, cudaStream_t s);
 
 // The paged cache: k and v [num_pages, page, Hkv, D] (bf16, or e4m3 with one fp32 scale per row

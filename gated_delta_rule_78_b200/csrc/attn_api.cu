@@ -56,10 +56,7 @@ gdn2_status check_rope(int flags, gdn2_dtype dt, int N, int H, int Hkv, int D, i
         return GDN2_ERR_SHAPE;
     return GDN2_OK;
 }
-size_t rope_partial_bytes(int flags, int N, int D)
-{
-    return flags & GDN2_ROPE_RMSNORM ? (size_t)2 * rope_bwd_blocks(N) * D * sizeof(float) : 0;
-}
+size_t rope_partial_bytes(int blocks, int D) { return (size_t)2 * blocks * D * sizeof(float); }
 
 gdn2_status attn_fwd(gdn2_dtype dt, const SeqBatch &b, int H, int Hkv, int D, int window, float scale, const void *q,
                      const void *k, const void *v, void *o, float *lse, void *stream)
@@ -176,7 +173,7 @@ gdn2_status gdn2_qk_rope_bwd(int flags, gdn2_dtype dt, int N, int H, int Hkv, in
     if (st == GDN2_OK && rot > 0) st = check_ptrs({positions, inv_freq});
     if (st != GDN2_OK) return st;
     if (want_w) {
-        if (!workspace || ws_bytes < rope_partial_bytes(flags, N, D)) return GDN2_ERR_WORKSPACE;
+        if (!workspace || ws_bytes < rope_partial_bytes(rope_bwd_blocks(N), D)) return GDN2_ERR_WORKSPACE;
         if ((st = check_ptrs({workspace})) != GDN2_OK) return st;
     }
     RopeArgs a{};
@@ -191,7 +188,7 @@ gdn2_status gdn2_qk_rope_bwd(int flags, gdn2_dtype dt, int N, int H, int Hkv, in
 size_t gdn2_qk_rope_workspace_size(int flags, gdn2_dtype dt, int N, int H, int Hkv, int D)
 {
     if (check_rope(flags, dt, N, H, Hkv, D, 0, 0.f, 1.f) != GDN2_OK) return 0;
-    return rope_partial_bytes(flags, N, D);
+    return flags & GDN2_ROPE_RMSNORM ? rope_partial_bytes(rope_bwd_most_blocks(N), D) : 0;
 }
 
 gdn2_status gdn2_attn_fwd(gdn2_dtype dt, int B, int T, int H, int Hkv, int D, int window, float scale, const void *q,

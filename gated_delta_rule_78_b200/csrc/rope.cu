@@ -330,6 +330,12 @@ int device_sms()
 }
 
 int rope_bwd_blocks(long long n) { return n > 0 ? (int)rope_grid(n, kBwdPerSm) : 0; }
+// The grid falls where warps stop sharing a token (511 tokens 511 blocks, 512 tokens 64); from there on it grows.
+int rope_bwd_most_blocks(long long n)
+{
+    const int own = rope_bwd_blocks(n), shared = rope_bwd_blocks(n < kShareBelow ? n : kShareBelow - 1);
+    return own > shared ? own : shared;
+}
 
 cudaError_t launch_rope(bool bwd, bool fp32, const RopeArgs &a, cudaStream_t s)
 {

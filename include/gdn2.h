@@ -351,7 +351,8 @@ GDN2_API gdn2_status gdn2_prologue(int flags, gdn2_dtype dt, int N, int H, int D
  * The backward takes the gradients of q_out and k_out and the forward's inputs, and writes dq, dk and
  * the fp32 weight gradients [D] (each may be NULL: not wanted).  Without GDN2_ROPE_RMSNORM q, k and the
  * weight gradients are ignored.  dq may be d_q_out and dk d_k_out.  Workspace:
- * gdn2_qk_rope_workspace_size() bytes when a weight gradient is wanted, else NULL is accepted.
+ * gdn2_qk_rope_workspace_size() bytes when a weight gradient is wanted, else NULL is accepted.  The size
+ * for N rows serves every call of N rows or fewer.
  */
 typedef enum { GDN2_ROPE_RMSNORM = 1, GDN2_ROPE_INTERLEAVED = 2 } gdn2_rope_flags;
 

@@ -78,6 +78,25 @@ def test_rope_bwd_refusals(lib):
     assert rope_bwd(lib, rot=7) == SHAPE
 
 
+def test_rope_workspace_serves_smaller_batches(lib):
+    """A workspace sized for N rows is enough for fewer: the need of a call, found where it starts to be
+    refused, never exceeds the size of a larger one.  (An unaligned address is refused after the size.)"""
+    def need(n):
+        lo, hi = 0, 1 << 30  # the least size that is not refused
+        while lo < hi:
+            mid = (lo + hi) // 2
+            lo, hi = (lo, mid) if rope_bwd(lib, N=n, ws=MIS, nb=mid) == ALIGN else (mid + 1, hi)
+        return lo
+
+    last = 0
+    for n in (1, 63, 64, 65, 296, 297, 400, 511, 512, 513, 2047, 2048, 4096, 100000, 1 << 29):
+        size = lib.gdn2_qk_rope_workspace_size(1, BF16, n, 2, 1, 128)
+        assert last <= size and need(n) <= size, n
+        assert size == g.gdn2_qk_rope_workspace_size(torch.bfloat16, n, 2, 1, 128)
+        last = size
+    assert need(511) > need(512)  # what makes it worth a test
+
+
 def test_attention_refusals(lib):
     for f in (fwd, fwd_varlen):
         assert f(lib, dt=7) == DTYPE
