@@ -254,7 +254,8 @@ struct CachedPlan {
     int splits;
 };
 CachedPlan cached_plan(bool e4m3, int n, long long rows, int H, int Hkv, int window, long long capacity);
-size_t cached_workspace_bytes(long long rows, int H, int D, int splits);
+long long cached_most_parts(bool e4m3, int n, long long rows, int H, int Hkv, int window, long long capacity);
+size_t cached_workspace_bytes(long long parts, int H, int D);
 cudaError_t launch_attn_cached(const CachedArgs &a, bool tc, cudaStream_t s);
 cudaError_t launch_attn_cached_tc(const CachedArgs &a, cudaStream_t s);
 

@@ -269,14 +269,14 @@ size_t gdn2_attn_cached_workspace_size(gdn2_dtype dt, int N, int total_T, int H,
     if (check_attn(dt, total_T, H, Hkv, D, window, 1.f) != GDN2_OK || total_T == 0 ||
         check_cache(GDN2_CACHE_BF16, dt, N, total_T, Hkv, D, max_pages, 1, page_size) != GDN2_OK)
         return 0;
-    window = effective_window(window, (long long)max_pages * page_size);
-    size_t most = 0;  // for either type of cache
+    const long long capacity = (long long)max_pages * page_size;
+    window = effective_window(window, capacity);
+    long long most = 0;  // for either type of cache
     for (bool e4m3 : {false, true}) {
-        const CachedPlan plan = cached_plan(e4m3, N, total_T, H, Hkv, window, (long long)max_pages * page_size);
-        const size_t need = cached_workspace_bytes(total_T, H, D, plan.splits);
-        most = need > most ? need : most;
+        const long long parts = cached_most_parts(e4m3, N, total_T, H, Hkv, window, capacity);
+        most = parts > most ? parts : most;
     }
-    return most;
+    return cached_workspace_bytes(most, H, D);
 }
 
 gdn2_status gdn2_attn_cached(gdn2_cache_type type, gdn2_dtype dt, int N, int total_T, int H, int Hkv, int D,
@@ -293,8 +293,8 @@ gdn2_status gdn2_attn_cached(gdn2_cache_type type, gdn2_dtype dt, int N, int tot
     if (st != GDN2_OK) return st;
     window = effective_window(window, (long long)max_pages * page_size);
     const CachedPlan plan = cached_plan(type == GDN2_CACHE_E4M3, N, total_T, H, Hkv, window, (long long)max_pages * page_size);
-    const size_t need = cached_workspace_bytes(total_T, H, D, plan.splits);
-    if (need) {
+    if (plan.splits > 1) {
+        const size_t need = cached_workspace_bytes((long long)plan.splits * total_T, H, D);
         if (!workspace || ws_bytes < need) return GDN2_ERR_WORKSPACE;
         if ((st = check_ptrs({workspace})) != GDN2_OK) return st;
     }

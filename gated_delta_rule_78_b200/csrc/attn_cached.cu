@@ -617,6 +617,40 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 }  // namespace
 
+namespace {
+
+constexpr int kMostSplits = 256;
+// Packed rows a sequence and key head, on average, up to which the rows kernel runs (see cached_plan).
+long long rows_limit(bool e4m3) { return e4m3 ? 64 : 16; }
+// The keys that a sequence's new rows see at most.
+long long visible_keys(long long rows, int window, long long capacity)
+{
+    return window > 0 && window + rows < capacity ? window + rows : capacity;
+}
+int clamp_splits(long long want, long long most)
+{
+    if (want > most) want = most;
+    return (int)(want > kMostSplits ? kMostSplits : want < 1 ? 1 : want);
+}
+int rows_splits(long long n, int Hkv, long long keys)
+{
+    // Two waves of blocks (one sequence over 32768 keys: 1 wave 24, 2 24, 4 28), and ragged lengths: no block
+    // reads more than 2048 keys, as far as kMostSplits goes (64 sequences of 64 to 8192 keys, e4m3: 39; 1024 40;
+    // any number 55)
+    const long long two = ceil_div(2LL * device_sms(), n * Hkv), even = ceil_div(keys, 2048);
+    return clamp_splits(two > even ? two : even, keys / 256);
+}
+int tile_splits(long long n, long long rows, int G, int Hkv, long long keys)
+{
+    // As many parts as blocks run at once, if sequences are alike.  512 tokens over 32768 keys: 4 parts 132,
+    // 5 (a second wave) 193, 8 142; 128 tokens: 16 parts 51, 13 59, 8 72; 4 x 512 over 16384, 128 blocks
+    // of their own: 1 part 227, 2 252.
+    const long long blocks = n * ((rows * G + 256LL * n - 1) / (256LL * n)) * Hkv;
+    return clamp_splits(device_sms() / blocks, keys / 512);
+}
+
+}  // namespace
+
 // Measured with H = 16, Hkv = 4, D = 128, times in us with the join.
 CachedPlan cached_plan(bool e4m3, int n, long long rows, int H, int Hkv, int window, long long capacity)
 {
@@ -627,31 +661,38 @@ CachedPlan cached_plan(bool e4m3, int n, long long rows, int H, int Hkv, int win
     // tiles, 8 sequences over 8192 keys: 16 rows 40 and 59, 20 rows 52 and 42, 32 rows 58 and 43; 64 over 2048:
     // 32 rows 104 and 71 (but 2 over 2048: 16 and 18).  e4m3, whose bytes are half and whose tiles wait for their
     // conversion, 8 over 8192: 32 rows 49 and 102, 64 rows 80 and 103, 128 rows 144 and 104.
-    plan.tc = rows * G > (e4m3 ? 64LL : 16LL) * n;
-    const long long keys = window > 0 && window + rows < capacity ? window + rows : capacity;
-    if (plan.tc) {
-        // As many parts as blocks run at once, if sequences are alike.  512 tokens over 32768 keys: 4 parts 132,
-        // 5 (a second wave) 193, 8 142; 128 tokens: 16 parts 51, 13 59, 8 72; 4 x 512 over 16384, 128 blocks
-        // of their own: 1 part 227, 2 252.
-        const long long blocks = n * ((rows * G + 256LL * n - 1) / (256LL * n)) * Hkv, want = device_sms() / blocks;
-        plan.splits = (int)(want < keys / 512 ? want : keys / 512);
-    } else {
-        // Two waves of blocks (one sequence over 32768 keys: 1 wave 24, 2 24, 4 28), and ragged lengths: no block
-        // reads more than 2048 keys (64 sequences of 64 to 8192 keys, e4m3: 39; 1024 40; any number 55)
-        const long long blocks = (long long)n * Hkv;
-        long long want = ceil_div(2LL * device_sms(), blocks);
-        const long long even = ceil_div(keys, 2048);
-        if (want < even) want = even;
-        plan.splits = (int)(want < keys / 256 ? want : keys / 256);
-    }
-    if (plan.splits > 256) plan.splits = 256;
-    if (plan.splits < 1) plan.splits = 1;
+    plan.tc = rows * G > rows_limit(e4m3) * n;
+    const long long keys = visible_keys(rows, window, capacity);
+    plan.splits = plan.tc ? tile_splits(n, rows, G, Hkv, keys) : rows_splits(n, Hkv, keys);
     return plan;
 }
 
-size_t cached_workspace_bytes(long long rows, int H, int D, int splits)
+// Partial outputs and log-sums: `parts` (part, row) pairs, or none if there is one part only.
+size_t cached_workspace_bytes(long long parts, int H, int D) { return (size_t)parts * H * (D + 1) * sizeof(float); }
+
+// The most (part, row) pairs that any call of up to n sequences, `rows` rows and `capacity` positions plans.
+// Both kinds of splits grow with the keys, so with the rows where nothing else changes, and with the capacity.
+long long cached_most_parts(bool e4m3, int n, long long rows, int H, int Hkv, int window, long long capacity)
 {
-    return splits > 1 ? (size_t)splits * rows * H * (D + 1) * sizeof(float) : 0;
+    const int G = H / Hkv, sms = device_sms();
+    long long most = 0;
+    auto count = [&](long long r, long long splits) { most = splits > 1 && splits * r > most ? splits * r : most; };
+    // Rows kernel: x sequences take up to `limit` rows; more sequences have fewer parts, until two waves are one
+    // block each (a last x is the number of sequences itself), and no more rows once all are taken.
+    for (long long x = 1; x <= n; ++x) {
+        if (x * Hkv > 2LL * sms) x = n;
+        const long long limit = rows_limit(e4m3) * x / G, r = limit < rows ? limit : rows;
+        if (r > 0) count(r, rows_splits(x, Hkv, visible_keys(r, window, capacity)));
+        if (r == rows) break;
+    }
+    // Tiles: of all numbers of sequences one has the fewest blocks to the same rows; b blocks a key head hold up
+    // to 256 b rows, and leave one part each from half of the SMs on.
+    for (long long b = 1; b * Hkv <= sms / 2; ++b) {
+        const long long limit = 256 * b / G, r = limit < rows ? limit : rows;
+        if (r * G > rows_limit(e4m3)) count(r, tile_splits(1, r, G, Hkv, visible_keys(r, window, capacity)));
+        if (r == rows) break;
+    }
+    return most;
 }
 
 cudaError_t launch_attn_cached(const CachedArgs &a, bool use_tc, cudaStream_t s)

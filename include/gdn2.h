@@ -430,8 +430,12 @@ GDN2_API gdn2_status gdn2_cache_read(gdn2_cache_type type, gdn2_dtype dt, int N,
  * Attention of each sequence's newest tokens (one for a decode step, a chunk of a long prompt) over
  * the paged cache, which already holds them.  q, o: [total_T, H, D]; lse: fp32 [total_T, H] or NULL.
  * The query at position i sees the cached positions j <= i (and j > i - window), as gdn2_attn_fwd.
- *   workspace: gdn2_attn_cached_workspace_size() bytes (for either type of cache); 0 needs none (NULL allowed).  The calls that
- *   share one must be ordered, captured graphs among them.
+ *   workspace: gdn2_attn_cached_workspace_size() bytes, which serve every call of no more sequences,
+ *   tokens and pages a sequence with the same heads, window and page size, over either type of cache; 0
+ *   needs none (NULL allowed).  The calls that share one must be ordered, captured graphs among them.
+ *   The key axis is cut by capacity (max_pages * page_size, or the window), as lengths are on the device:
+ *   one part to 2048 keys of it, 256 parts at most, each of (D + 1) floats to a token and head.  So the
+ *   workspace of a large batch grows with max_pages.
  */
 GDN2_API gdn2_status gdn2_attn_cached(gdn2_cache_type type, gdn2_dtype dt, int N, int total_T, int H, int Hkv, int D,
                                       int window, float scale, const int *cu_seqlens, const int *kv_lens,

@@ -148,6 +148,34 @@ def test_cached_attention_refusals(lib):
     assert lib.gdn2_attn_cached_workspace_size(BF16, 1, 1, 2, 1, 128, 64, 4096, 16) == 0
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that needs no workspace would launch on the stand-in addresses")
+@pytest.mark.parametrize("H,Hkv", [(16, 4), (8, 8), (64, 1), (6, 2)])
+@pytest.mark.parametrize("window", [0, 2048])
+def test_cached_workspace_serves_smaller_calls(lib, window, H, Hkv):
+    """A workspace sized for a call is enough for every call of fewer sequences, tokens and pages, over
+    either type of cache.  (A misaligned address is refused after the size; without a device, a call that
+    needs none ends at the status word.)"""
+    def need(kind, n, t, width):
+        lo, hi = 0, 1 << 40
+        if cached(lib, kind, N=n, T=t, H=H, Hkv=Hkv, window=window, width=width, ks=P, vs=P, ws=NUL, nb=0) != WS:
+            return 0
+        while lo < hi:
+            mid = (lo + hi) // 2
+            ok = cached(lib, kind, N=n, T=t, H=H, Hkv=Hkv, window=window, width=width, ks=P, vs=P, ws=MIS, nb=mid) == ALIGN
+            lo, hi = (lo, mid) if ok else (mid + 1, hi)
+        return lo
+
+    ns, ts, widths = [1, 2, 3, 5, 37, 75, 256], [1, 2, 4, 7, 16, 17, 64, 65, 130, 256, 300, 513, 2048], [4, 150, 1024, 8192]
+    size = {(n, t, w): lib.gdn2_attn_cached_workspace_size(BF16, n, t, H, Hkv, 128, window, w, 16) for n in ns for t in ts for w in widths}
+    needs = {(n, t, w): max(need(kind, n, t, w) for kind in (0, 1)) for n in ns for t in ts for w in widths}
+    some = 0
+    for (n, t, w), have in size.items():
+        most = max(v for (a, b, c), v in needs.items() if a <= n and b <= t and c <= w)
+        assert most <= have, (n, t, w)
+        some += needs[n, t, w] < most
+    assert some > 0  # calls that need less than a smaller one are what makes it worth a test
+
+
 def test_status_names(lib):
     assert g.STATUS_NAMES[-11] == "GDN2_ERR_PAGES" and b"paged" in lib.gdn2_strerror(-11)
 

@@ -307,3 +307,23 @@ def test_pages_behind_the_window(cuda_lib, page, rows, window, D, e4m3):
         assert g.gdn2_sync_status() == 0, entry
         for x, y in zip(got, want):
             assert torch.equal(x, y), entry
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+def test_one_workspace_for_smaller_calls(cuda_lib, e4m3):
+    """A server's workspace, sized once for its largest call: chunks and single tokens of fewer sequences
+    over shorter tables give the same with it as with one of their own."""
+    g = cuda_lib
+    H, Hkv, page = 16, 4, 16
+    size = g.gdn2_attn_cached_workspace_size(4, 2048, H, Hkv, 64, 0, 512, page)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    for q_lens, width in (([512] * 4, 512), ([1] * 4, 512), ([1], 512), ([60], 512), ([30, 1], 200), ([1] * 3, 40)):
+        b = Batch(q_lens, [n + 230 + 50 * i for i, n in enumerate(q_lens)], page, Hkv, 64, e4m3, seed=width).fill(g)
+        d = b.dev
+        d["table"] = torch.nn.functional.pad(b.table, (0, width - b.table.shape[1]), value=-5).cuda()
+        q = torch.randn(b.total, H, 64, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+        ws.fill_(255)  # NaN
+        want = g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args())
+        got = g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args(), workspace=ws)
+        assert g.gdn2_sync_status() == 0
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), (q_lens, width)
