@@ -157,7 +157,8 @@ inline long long tile_bound(const SeqBatch &b, int per)
     return b.cu ? b.rows / per + b.n : (long long)b.n * ((b.T + per - 1) / per);
 }
 // The sequence that holds row t, by a whole warp: 32 boundaries at a time, a ballot a step.
-// -1 for rows behind the last sequence and for an invalid cu around t.
+// -1 for rows behind the last sequence and for an invalid cu around t.  An entry outside [0, rows] may lead the
+// ballots to a sequence that it makes invalid, from any row: then all are looked through, a step of 32 each.
 __device__ __forceinline__ int find_seq(const SeqBatch &b, int t, SeqSpan &sp)
 {
     const int lane = threadIdx.x & 31;
@@ -173,6 +174,15 @@ __device__ __forceinline__ int find_seq(const SeqBatch &b, int t, SeqSpan &sp)
     }
     // sequences of no tokens share their start with the one after them, which the last ballot took
     sp = batch_span(b, lo);
+    for (int base = 0; sp.len < 0 && base < b.n; base += 32) {
+        SeqSpan x = {0, -1};
+        if (base + lane < b.n) x = batch_span(b, base + lane);
+        const unsigned hit = __ballot_sync(0xffffffffu, x.len > 0 && t >= x.bos && t - x.bos < x.len);
+        if (!hit) continue;
+        lo = base + __ffs(hit) - 1;
+        sp.bos = __shfl_sync(0xffffffffu, x.bos, lo - base);
+        sp.len = __shfl_sync(0xffffffffu, x.len, lo - base);
+    }
     return sp.len > 0 && t >= sp.bos && t < sp.bos + sp.len ? lo : -1;
 }
 

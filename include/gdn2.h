@@ -328,8 +328,9 @@ GDN2_API gdn2_status gdn2_prologue(int flags, gdn2_dtype dt, int N, int H, int D
  *    < 2^31 (GDN2_ERR_UNSUPPORTED beyond).
  *  - Packed batches: cu_seqlens, DEVICE int32 [N + 1], 0 = c_0 <= c_1 <= ... <= c_N <= total_T.
  *    Empty sequences are allowed; rows behind c_N belong to no sequence and the outputs' rows there
- *    are left as they were (a padded batch).  A sequence whose entries are invalid is skipped, its
- *    outputs left as they were, and GDN2_ERR_SEQLENS recorded.
+ *    are left as they were (a padded batch).  A sequence whose entries are invalid (outside 0 ..
+ *    total_T, or falling) is skipped, its outputs left as they were, and GDN2_ERR_SEQLENS recorded.
+ *    Outputs of rows that entries out of order give to two sequences are undefined.
  *  - q, k, v and d_o of a sequence are expected to be finite.  A value that is not may reach the
  *    outputs of any token of its own sequence, those that mask it included, but never those of
  *    another sequence; what lies behind a sequence in its last page is never used.

@@ -327,3 +327,35 @@ def test_one_workspace_for_smaller_calls(cuda_lib, e4m3):
         got = g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args(), workspace=ws)
         assert g.gdn2_sync_status() == 0
         assert all(torch.equal(x, y) for x, y in zip(got, want)), (q_lens, width)
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+@pytest.mark.parametrize("most", [1, 90])
+def test_invalid_sequences_are_skipped(cuda_lib, most, e4m3):
+    """Invalid cu_seqlens entries in a batch of many sequences: the two around one are skipped by every
+    call of the cache, the others are as without it, in one part and in several."""
+    g = cuda_lib
+    H = 4
+    for entry in (-1, 2 ** 31 - 1):
+        q_lens = [1 + (i % 3) * (most // 3) for i in range(45)]
+        kv = [n + 20 * (i % 4) + (2500 if i == 7 else 0) for i, n in enumerate(q_lens)]
+        b = Batch(q_lens, kv, 16, 2, 64, e4m3, seed=most).fill(g)
+        cu = R.lens_to_cu(q_lens)
+        skipped = torch.zeros(b.total, dtype=torch.bool)
+        skipped[cu[35]:cu[37]] = True
+        cu[36] = entry
+        q = torch.randn(b.total, H, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+        d = b.dev
+        want = g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args())
+        want_kv = g.gdn2_cache_read(d["kc"], d["vc"], *b.args(), total_T=b.total)
+        assert g.gdn2_sync_status() == 0
+        d["cu"] = cu.cuda()
+        o, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+        g.gdn2_attn_cached(q, d["kc"], d["vc"], *b.args(), o=o, lse=lse)
+        assert g.gdn2_sync_status() == -10
+        kb, vb = (torch.full((b.total, 2, 64), 7.0).bfloat16().cuda() for _ in range(2))
+        g.gdn2_cache_read(d["kc"], d["vc"], *b.args(), k=kb, v=vb)
+        assert g.gdn2_sync_status() == -10
+        for got, ref in zip((o, lse, kb, vb), (*want, *want_kv)):
+            got, ref = got.cpu(), ref.cpu()
+            assert (got[skipped] == 7.0).all() and torch.equal(got[~skipped], ref[~skipped])
