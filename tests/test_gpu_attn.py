@@ -216,3 +216,52 @@ def test_streams_and_graphs(cuda_lib):
     torch.cuda.synchronize()
     for n, t in (("o", o), ("lse", lse), *grads.items()):
         assert torch.equal(t, want[n]), n
+
+
+BAD_SEQLENS = [
+    # entries, rows, the sequences that are valid by their own two entries
+    ([0, 150, 100], [(0, 150)]),
+    ([0, 100, 201], [(0, 100)]),
+    ([3, 100, 200], [(100, 100)]),
+    ([0, -5, 100, 200], [(100, 100)]),
+    ([0, 40, 2 ** 31 - 1, 200], [(0, 40)]),
+    ([0, -2 ** 31, -2 ** 31], []),
+    # more sequences than a warp looks up at a time, an entry in the middle
+    ([0] + [5 * i if i != 21 else -1 for i in range(1, 41)], [(5 * i, 5) for i in range(40) if i not in (20, 21)]),
+    ([0] + [5 * i if i != 37 else 201 for i in range(1, 41)], [(5 * i, 5) for i in range(40) if i not in (36, 37)]),
+]
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("window", [0, 30])
+@pytest.mark.parametrize("case", range(len(BAD_SEQLENS)))
+def test_invalid_sequences_are_skipped(cuda_lib, case, window, dt):
+    """Forward and backward leave the rows of a sequence with invalid entries as they were; the valid ones
+    are as without it."""
+    g = cuda_lib
+    entries, spans = BAD_SEQLENS[case]
+    x, _ = make([200], 4, 2, 64, dt, seed=case)
+    d = {n: t.cuda() for n, t in x.items()}
+    cu = torch.tensor(entries, dtype=torch.int32, device="cuda")
+    o, lse = torch.full_like(d["q"], 7.0), torch.full(d["q"].shape[:2], 7.0, device="cuda")
+    g.gdn2_attn_fwd_varlen(d["q"], d["k"], d["v"], cu, window=window, scale=0.125, o=o, lse=lse)
+    assert g.gdn2_sync_status() == -10
+    out = {"dq": torch.full_like(d["q"], 7.0), "dk": torch.full_like(d["k"], 7.0), "dv": torch.full_like(d["v"], 7.0)}
+    g.gdn2_attn_bwd_varlen(d["q"], d["k"], d["v"], o, lse, d["do"], cu, window=window, scale=0.125, out=out)
+    assert g.gdn2_sync_status() == -10
+    skipped = torch.ones(200, dtype=torch.bool)
+    for b, n in spans:
+        skipped[b:b + n] = False
+    got = {"o": o, "lse": lse, **out}
+    for n, t in got.items():
+        assert (t.cpu()[skipped] == 7.0).all(), n
+    compare(got, x, spans, window, 0.125)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,Hkv,window", [(16, 16, 0), (32, 16, 0), (16, 16, 45)])
+def test_fp32_batches_that_fill_the_device(cuda_lib, H, Hkv, window, D):
+    """fp32 keys by 32 to a block, which batches of at least two blocks to an SM take."""
+    lens = [333, 1, 260, 47]
+    x, spans = make(lens, H, Hkv, D, torch.float32, seed=D + H)
+    compare(run_packed(cuda_lib, x, lens, window, D ** -0.5), x, spans, window, D ** -0.5)

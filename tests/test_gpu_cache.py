@@ -329,6 +329,88 @@ def test_one_workspace_for_smaller_calls(cuda_lib, e4m3):
         assert all(torch.equal(x, y) for x, y in zip(got, want)), (q_lens, width)
 
 
+@pytest.mark.parametrize("D,Hkv", [(128, 8), (64, 5), (128, 3)])
+def test_write_e4m3_prompts(cuda_lib, D, Hkv):
+    """Enough rows (more than 4096 warp passes) that a warp takes several passes of a token's heads."""
+    g = cuda_lib
+    b = Batch([700, 0, 811, 3], [700, 5, 900, 3], 16, Hkv, D, True, seed=D + Hkv).fill(g)
+    d = b.dev
+    k, v = g.gdn2_cache_read(d["kc"], d["vc"], R.lens_to_cu(b.kv).cuda(), d["kv"], d["table"], d["ks"], d["vs"], total_T=sum(b.kv))
+    assert g.gdn2_sync_status() == 0
+    for got, ref in zip((k, v), [torch.cat(x) for x in zip(*[b.held(i) for i in range(4)])]):
+        assert torch.equal(got.cpu(), ref.float().bfloat16())
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+@pytest.mark.parametrize("window", [0, 33])
+@pytest.mark.parametrize("most", [1, 3, 90])
+def test_many_sequences(cuda_lib, most, window, e4m3):
+    """More sequences than a warp looks up at a time, empty ones among them: single tokens, some with more
+    (further tiles of the rows kernel), and mostly chunks (tiles of the tensor core), in one part and in several."""
+    order = random.Random(most)
+    q_lens = [order.choice([0, 1, 1, most]) for _ in range(75)]
+    q_lens[40], q_lens[70] = max(most, 13), 1
+    kv = [n + order.choice([0, 5, 130, 400]) for n in q_lens]
+    kv[70] = 3000
+    b = Batch(q_lens, kv, 16, 1, 64, e4m3, seed=most, tail=2).fill(cuda_lib)
+    verify(b, *attend(cuda_lib, b, 4, window=window), 4, window, 0.11)
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+@pytest.mark.parametrize("page", [16, 7])
+@pytest.mark.parametrize("rows", [1, 100])
+def test_rows_of_bad_pages(cuda_lib, rows, page, e4m3):
+    """A page outside the cache: its rows are skipped by write and read, and attention reads zeros for
+    them (a score of 0 and nothing of its value); the rows of other pages are as always."""
+    g = cuda_lib
+    for bad in (-1, 10 ** 9, -2 ** 31):
+        b = Batch([rows, rows], [rows + 40, rows + 90], page, 2, 64, e4m3, seed=page + rows).fill(g)
+        d = b.dev
+        lost = [(1, 2), (1, (rows + 89) // page)]  # a page of the past, and the last, which holds new rows
+        if rows > 1:
+            lost.append((0, (40 + rows // 2) // page))
+        gone = [torch.zeros(n, dtype=torch.bool) for n in b.kv]
+        table = b.table.clone()
+        for i, pg in lost:
+            table[i, pg] = bad
+            gone[i][pg * page:(pg + 1) * page] = True
+        d["table"] = table.cuda()
+        # attention, against the cache with zeros there
+        q, o, lse = torch.randn(b.total, 4, 64).bfloat16(), None, None
+        o, lse = g.gdn2_attn_cached(q.cuda(), d["kc"], d["vc"], *b.args(), scale=0.11)
+        assert g.gdn2_sync_status() == -11
+        for i in range(2):
+            at = slice(i * rows, (i + 1) * rows)
+            k, v = (t.clone() for t in b.held(i))
+            k[gone[i]], v[gone[i]] = 0, 0
+            for h in range(4):
+                x = R.head(q[at, h], k[:, h // 2], v[:, h // 2], b.kv[i] - rows, 0, 0.11, torch.bfloat16)
+                R.check(o[at, h], x["o"], x["o_tol"], "o")
+                R.check(lse[at, h], x["lse"], x["lse_tol"], "lse")
+        # reading the new rows
+        kb, vb = (torch.full((b.total, 2, 64), 7.0).bfloat16().cuda() for _ in range(2))
+        g.gdn2_cache_read(d["kc"], d["vc"], *b.args(), k=kb, v=vb)
+        assert g.gdn2_sync_status() == -11
+        new_gone = torch.cat([gone[i][b.kv[i] - rows:] for i in range(2)])
+        assert new_gone.any()
+        for got, which in ((kb.cpu(), 0), (vb.cpu(), 1)):
+            ref = torch.cat([b.held(i)[which][b.kv[i] - rows:] for i in range(2)]).float().bfloat16()
+            assert (got[new_gone] == 7.0).all() and torch.equal(got[~new_gone], ref[~new_gone])
+        # writing others in their place
+        before = [d[n].view(torch.uint8).cpu().flatten(2) for n in ("kc", "vc")]
+        fresh = torch.randn(b.total, 2, 64).bfloat16().cuda()
+        g.gdn2_cache_write(fresh, -fresh, d["kc"], d["vc"], *b.args())
+        assert g.gdn2_sync_status() == -11
+        written = torch.zeros(b.kc.shape[:2], dtype=torch.bool)
+        for i in range(2):
+            for p in range(b.kv[i] - rows, b.kv[i]):
+                if not gone[i][p]:
+                    written[b.table[i, p // page], p % page] = True
+        for was, n in zip(before, ("kc", "vc")):
+            same = (was == d[n].view(torch.uint8).cpu().flatten(2)).all(-1)
+            assert same[~written].all() and not same[written].any()
+
+
 @pytest.mark.parametrize("e4m3", KINDS)
 @pytest.mark.parametrize("most", [1, 90])
 def test_invalid_sequences_are_skipped(cuda_lib, most, e4m3):

@@ -182,3 +182,11 @@ def test_far_scales_without_eps(cuda_lib, flags, dt):
         x[n] *= torch.logspace(15, -16, 9)[:, None, None]
     x = {n: t.to(dt) if n in ("q", "k", "dq", "dk") else t for n, t in x.items()}
     verify(x, flags, run(cuda_lib, x, flags, eps=0.0), eps=0.0)
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N", [511, 512, 513])
+def test_rows_where_warps_stop_sharing(cuda_lib, N, dt):
+    """The warps of a block share a token's heads below 512 tokens."""
+    x = make(N, 19, 2, 64, 64, dt, seed=N)
+    verify(x, 1, run(cuda_lib, x, 1))
