@@ -66,9 +66,10 @@ __device__ __forceinline__ float sum_of(uint64_t x)
     return a + b;
 }
 
-// cos and sin of pos * inv, times f.  The product of an int and a float is exact in 64 bits, and so
-// is the angle modulo a turn to about 1e-12; the remainder lies in [-pi, pi], where sincosf needs
-// no long reduction.
+// cos and sin of pos * inv, times f.  The product of an int and a float is exact in 64 bits for positions below
+// 2^29, beyond them off by 2^-53 of itself.  The rounded 2 pi adds 2.5e-16 a turn: 4e-12 at an angle of 10^5, 8e-8
+// at 2^31, where the product's 1.2e-7 comes on top.  The remainder lies in [-pi, pi], where sincosf needs no long
+// reduction.
 __device__ __forceinline__ void angle(int pos, float inv, float f, float &c, float &s)
 {
     const double a = (double)pos * (double)inv;
@@ -239,14 +240,14 @@ __global__ void __launch_bounds__(kWarps * 32, bwd ? 2 : 3) rope_kernel(const Ro
                                 d2 = fma2(ux, wt[e], d2);
                             }
                         }
-                        if (a.norm) {  // dx = r (u w - x (r^2 / D sum u w x)): r^3 leaves fp32's range where r does not
+                        if (a.norm) {  // dx = u (r w) - x (r^3 / D sum u w x); r^3 alone leaves fp32's range where r does not
                             float dot = sum_of(d2);
 #pragma unroll
                             for (int m = L / 2; m >= 1; m >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-                            dot *= -r * r * (1.f / D);
+                            dot = dot * r * r * r * (-1.f / D);
                             const uint64_t k2 = pair(dot, dot);
 #pragma unroll
-                            for (int e = 0; e < P; ++e) u2[e] = mul2(fma2(f[e], k2, mul2(u2[e], wt[e])), r2);
+                            for (int e = 0; e < P; ++e) u2[e] = fma2(u2[e], mul2(wt[e], r2), mul2(f[e], k2));
                         }
                         if (h < heads) *reinterpret_cast<uint4 *>(y + (size_t)h * D) = pack(u2);
                     }
