@@ -9,7 +9,7 @@
 // (3 products a tile pair); one block to 128 keys of a key head walks over the packed query rows of
 // all of its query heads and keeps dk and dv in TMEM (4 products a tile pair).  One kernel with dq
 // accumulated in memory would need 5 products a pair instead of 7, and fp32 atomics.  p and ds are
-// rounded to bf16 for their products (2^-9 of each term), everything else is fp32.
+// rounded to bf16 for their products (up to 2^-8 of each term), everything else is fp32.
 //
 // o comes rounded to bf16, and what that does to delta is a fixed share of p in every ds of a row, which
 // does not average out; most in a sequence's first rows, whose few weights are large.  Where all keys of

@@ -22,7 +22,7 @@
 // Cut into parts, each part writes its normalised output and log-sum; a second kernel joins them,
 // in a fixed order.
 //
-// 256 sequences of 256 to 8192 keys, 16 heads on 4, D = 128, e4m3: 129 us and 5 for the joining (4.7 TB/s; sequences
+// 256 sequences of 256 to 8192 keys, 16 heads on 4, D = 128, e4m3: 129 us with the joining's 5 (4.7 TB/s; sequences
 // alike, 2048 keys each: 98 us).  One sequence over 32768 keys, bf16: 18.5 and 5 us, launch and latency.
 #include "attn_tc.cuh"
 
@@ -651,7 +651,7 @@ int tile_splits(long long n, long long rows, int G, int Hkv, long long keys)
 
 }  // namespace
 
-// Measured with H = 16, Hkv = 4, D = 128, times in us with the join.
+// Measured with H = 16, Hkv = 4, D = 128, times in us with the join; D = 64 and other groups go by the same rules.
 CachedPlan cached_plan(bool e4m3, int n, long long rows, int H, int Hkv, int window, long long capacity)
 {
     const int G = H / Hkv;

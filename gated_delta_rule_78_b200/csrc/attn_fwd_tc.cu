@@ -7,7 +7,7 @@
 // maximum only when a row's maximum has grown by more than 2^8 since: sums and outputs then stay
 // far from overflow in fp32, and the accumulator is rescaled a few times a row instead of once a
 // tile.  The weights are rounded to bf16 for the second product (their sum l_i is of the unrounded
-// ones); that costs 2^-9 of each weight, no more than the rounding of o.
+// ones); that costs up to 2^-8 of each weight, no more than the rounding of o.
 //
 // A block owns two tiles A and B of 128 packed query rows.  Roles: warps 0-3 and 4-7 the softmax of
 // A and of B (a thread to a row), warp 8 the products, warp 9 the TMA loads, warps 9-11 (paged)

@@ -333,7 +333,8 @@ GDN2_API gdn2_status gdn2_prologue(int flags, gdn2_dtype dt, int N, int H, int D
  *    Outputs of rows that entries out of order give to two sequences are undefined.
  *  - q, k, v and d_o of a sequence are expected to be finite.  A value that is not may reach the
  *    outputs of any token of its own sequence, those that mask it included, but never those of
- *    another sequence; what lies behind a sequence in its last page is never used.
+ *    another sequence; what lies behind a sequence in its last page is never used.  Scores are expected
+ *    to be finite too: the outputs of a row whose q . k overflow fp32 are unspecified.
  *  - Every result is the same from call to call, bit for bit: no sum depends on timing.
  */
 
@@ -350,10 +351,10 @@ GDN2_API gdn2_status gdn2_prologue(int flags, gdn2_dtype dt, int N, int H, int D
  *   rot_scale.  The angle is formed in 64 bits, so positions may be far.
  * q_out may be q and k_out k.  Asynchronous on `stream`.
  * The backward takes the gradients of q_out and k_out and the forward's inputs, and writes dq, dk and
- * the fp32 weight gradients [D] (each may be NULL: not wanted).  Without GDN2_ROPE_RMSNORM q, k and the
- * weight gradients are ignored.  dq may be d_q_out and dk d_k_out.  Workspace:
- * gdn2_qk_rope_workspace_size() bytes when a weight gradient is wanted, else NULL is accepted.  The size
- * for N rows serves every call of N rows or fewer.
+ * the weight gradients, fp32 [D] and summed in fp32 (either may be NULL: not wanted).  Without
+ * GDN2_ROPE_RMSNORM q, k and the weight gradients are ignored.  dq may be d_q_out and dk d_k_out.
+ * Workspace: gdn2_qk_rope_workspace_size() bytes when a weight gradient is wanted, else NULL is accepted;
+ * the size for N rows serves every call of N rows or fewer.
  */
 typedef enum { GDN2_ROPE_RMSNORM = 1, GDN2_ROPE_INTERLEAVED = 2 } gdn2_rope_flags;
 
@@ -375,7 +376,8 @@ GDN2_API size_t gdn2_qk_rope_workspace_size(int flags, gdn2_dtype dt, int N, int
  *   q, o: [B, T, H, D]; k, v: [B, T, Hkv, D] of type dt (packed: [total_T, ..]); scale > 0.
  *   lse: fp32 [B, T, H], or NULL when not wanted.
  * bf16 runs on the tensor cores (fp32 scores, sums and accumulators; the weights p rounded to bf16
- * for the second product), fp32 in fp32 throughout.
+ * for the second product), fp32 in fp32 throughout.  The bf16 backward rounds p and
+ * ds = p (d_o . v - d_o . o) to bf16 for their products, and sees o as it was stored.
  * The backward of L = <o, d_o>, given the forward's inputs, o and lse:
  *   dq, dk, dv as q, k, v; gradients of a key head are sums over its query heads.
  *   workspace: gdn2_attn_workspace_size() bytes (packed: N = 1, T = total_T).

@@ -201,3 +201,32 @@ def test_a_planted_mistake_in_the_chain_is_caught():
     ref = oracle.ref_bwd(*(as_bthd(x[n]) for n in "qkvgbw"), x["S"][None, None], as_bthd(x["dO"]),
                          x["dSn"][None, None])["dS0"][0, 0]
     assert np.abs(wrong - ref).max() > 1e-3 * np.abs(ref).max()
+
+
+# ------------------------------------------------------------------ the attention backward's exponentials
+def ex2_fma(x):
+    """2^x in fp32 as the kernels form a part of their weights: the nearest integer by adding 1.5 * 2^23, a
+    polynomial of degree 5 for the rest, the integer added to the exponent.  fp64 holds each product exactly,
+    so an FMA is its sum rounded (twice, in rare cases) to fp32."""
+    k = [1.0, 0.693147182, 0.240221068, 0.0555035695, 0.00967603177, 0.00133908633]
+    f32 = np.float32
+    fma = lambda a, b, c: (a.astype(np.float64) * np.float64(b) + np.float64(c)).astype(f32)  # noqa: E731
+    x = np.maximum(x.astype(f32), f32(-126))
+    t = x + f32(12582912)
+    n = t - f32(12582912)
+    f = fma(n, -1.0, x)
+    y = np.full_like(x, k[5])
+    for c in k[4::-1]:
+        y = (y.astype(np.float64) * f + f32(c)).astype(f32)
+    return (y.view(np.int32) + (t.view(np.int32) << 23)).view(f32)
+
+
+def test_exponential_on_the_fma_pipe():
+    """Within the polynomial's 2.1e-7 and one fp32 half step (6e-8) of its last operation, the second last's
+    being halved by |f| <= 1/2; whole powers are exact, and what lies below 2^-126 becomes it."""
+    x = np.concatenate([np.linspace(-126, 127, 2000003), np.linspace(-0.5, 0.5, 1000003)]).astype(np.float32)
+    y = ex2_fma(x).astype(np.float64)
+    assert np.abs(y / np.exp2(x.astype(np.float64)) - 1).max() <= 2.1e-7 + 1.5 * 2.0 ** -24
+    n = np.arange(-126, 128, dtype=np.float32)
+    assert np.array_equal(ex2_fma(n), np.ldexp(np.float32(1), n.astype(int)))
+    assert np.array_equal(ex2_fma(np.array([-127, -1000, -np.inf], np.float32)), np.full(3, 2.0 ** -126, np.float32))
