@@ -441,3 +441,36 @@ def test_invalid_sequences_are_skipped(cuda_lib, most, e4m3):
         for got, ref in zip((o, lse, kb, vb), (*want, *want_kv)):
             got, ref = got.cpu(), ref.cpu()
             assert (got[skipped] == 7.0).all() and torch.equal(got[~skipped], ref[~skipped])
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+@pytest.mark.parametrize("window", [0, 200])
+@pytest.mark.parametrize("n,rows", [(3, 1), (70, 1), (2, 90)])
+def test_tables_far_wider_than_the_sequences(cuda_lib, n, rows, window, e4m3):
+    """A table for 131072 positions, as a server or a captured graph has it: most parts of the key axis are
+    empty, and few or many rows are joined over them."""
+    g = cuda_lib
+    kv = [rows + (997 * i) % 1500 for i in range(n)]
+    b = Batch([rows] * n, kv, 16, 2, 64, e4m3, seed=n).fill(g)
+    b.dev["table"] = torch.nn.functional.pad(b.table, (0, 8192 - b.table.shape[1]), value=-5).cuda()
+    assert g.gdn2_attn_cached_workspace_size(n, n * rows, 16, 2, 64, 0, 8192, 16) > 0
+    verify(b, *attend(g, b, 16, window=window), 16, window, 0.11)
+
+
+@pytest.mark.parametrize("e4m3", KINDS)
+@pytest.mark.parametrize("rows", [1, 70])
+@pytest.mark.parametrize("big_q,big_k,big_v", [(1e-20, 1e20, 1.0), (1e20, 1e-20, 1e30), (1.0, 1.0, 1e-30), (30.0, 1.0, 1.0)])
+def test_far_scales(cuda_lib, big_q, big_k, big_v, rows, e4m3):
+    """Queries, keys and values far from 1 whose scores are not, values whose rows differ by 1e6 in scale, and
+    scores of hundreds."""
+    g = cuda_lib
+    b = Batch([rows, rows], [rows + 300, rows + 4000], 16, 2, 64, e4m3, seed=9)
+    gen = torch.Generator().manual_seed(7)
+    b.k_all = [(big_k * x.float()).bfloat16() for x in b.k_all]
+    b.v_all = [(big_v * x.float() * 10.0 ** torch.randint(-3, 4, (len(x), 1, 1), generator=gen)).bfloat16() for x in b.v_all]
+    b.fill(g)
+    d = b.dev
+    q = (big_q * torch.randn(b.total, 8, 64, generator=gen)).bfloat16()
+    o, lse = g.gdn2_attn_cached(q.cuda(), d["kc"], d["vc"], *b.args(), scale=0.11)
+    assert g.gdn2_sync_status() == 0
+    verify(b, q, o, lse, 8, 0, 0.11)
